@@ -17,6 +17,7 @@ the kernels: raw q/k rows are L2-normalised, alpha/beta are given as logits.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -32,7 +33,12 @@ _STATUS = {0: "GDN_OK", 1: "GDN_ERR_NULL_POINTER", 2: "GDN_ERR_BAD_SHAPE",
            6: "GDN_ERR_HIP"}
 EXPORTS = ("gdn_prefill_chunked", "gdn_decode_step", "gdn_varlen_prefill", "gdn_decode_multi",
            "gdn_prefill_workspace_size", "gdn_status_string", "gdn_version",
-           "gdn_prefill_chunked_noalloc")
+           "gdn_prefill_chunked_noalloc", "gdn_scan_prefill", "gdn_scan_varlen_prefill",
+           "gdn_scan_backward", "gdn_scan_varlen_backward", "gdn_scan_decode",
+           "gdn_scan_workspace_size", "gdn_rms_norm", "gdn_rms_norm_backward",
+           "gdn_rms_norm_workspace_size", "gdn_beam_select", "gdn_beam_workspace_size",
+           "gdn_gather_states")
+SCAN_TILE = 128  # prefix states that gdn_scan_backward needs: every 64 or 128 tokens
 
 _lib = None
 
@@ -76,6 +82,31 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.gdn_status_string.restype = ctypes.c_char_p
     lib.gdn_version.argtypes = []
     lib.gdn_version.restype = i32
+    ci = ctypes.c_int
+    lib.gdn_scan_prefill.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i64, i32, ci, u32, vp,
+                                     sz, vp]
+    lib.gdn_scan_varlen_prefill.argtypes = [vp, vp, vp, vp, i32, i64, vp, vp, vp, vp, i32, i32, ci,
+                                            u32, vp, sz, vp]
+    lib.gdn_scan_backward.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, i32, i64,
+                                      i32, ci, u32, vp, sz, vp]
+    lib.gdn_scan_varlen_backward.argtypes = [vp, vp, vp, vp, vp, i32, i64, vp, vp, i32, vp, vp, vp,
+                                             vp, vp, i32, ci, u32, vp, sz, vp]
+    lib.gdn_scan_decode.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp, i32, i32, i32, ci, u32, vp]
+    lib.gdn_scan_workspace_size.argtypes = [i32, i64, i32, ci, i32]
+    lib.gdn_rms_norm.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i64, i32, ci, f32, vp]
+    lib.gdn_rms_norm_backward.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, ci, f32, vp, sz, vp]
+    lib.gdn_rms_norm_workspace_size.argtypes = [i64, i32]
+    lib.gdn_beam_select.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i64, i32, ci, vp,
+                                    sz, vp]
+    lib.gdn_beam_workspace_size.argtypes = [i32, i32, i64, ci]
+    lib.gdn_gather_states.argtypes = [vp, i64, vp, vp, i64, i64, vp]
+    for name in ("gdn_scan_prefill", "gdn_scan_varlen_prefill", "gdn_scan_backward",
+                 "gdn_scan_varlen_backward", "gdn_scan_decode", "gdn_rms_norm",
+                 "gdn_rms_norm_backward", "gdn_beam_select", "gdn_gather_states"):
+        getattr(lib, name).restype = ci
+    for name in ("gdn_scan_workspace_size", "gdn_rms_norm_workspace_size",
+                 "gdn_beam_workspace_size"):
+        getattr(lib, name).restype = sz
     _lib = lib
     return lib
 
@@ -330,6 +361,399 @@ def gdn_decode_multi(q, k, v, alpha, beta, state_pool, src_slot, dst_slot, *, ou
         state_pool.shape[0], _ptr(src_slot), _ptr(dst_slot), _ptr(out), _ptr(step_states), B, K,
         Hk, Hv, Dk, Dv, _dtype_code(q), float(scale), int(flags), _stream(dev, stream).cuda_stream))
     return out, step_states
+
+
+class _On:
+    """Device and stream of one call: torch allocates and the library launches
+    there, whatever the current device and stream are."""
+
+    def __init__(self, dev, stream):
+        if dev.type != "cuda":
+            raise ValueError(f"tensors must be on a GPU, got {dev}")
+        self.stream = stream if stream is not None else torch.cuda.current_stream(dev)
+        self._outer = None
+        if stream is not None or torch.cuda.current_device() != dev.index:
+            self._outer = torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        if self._outer is not None:
+            self._outer.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self._outer is not None:
+            self._outer.__exit__(*exc)
+
+
+def _dims(t, name, n):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _opt(t, name, dtype, shape, device):
+    if t is not None:
+        _need(t, name, dtype, shape, device)
+
+
+def _scratch(workspace, size, dev, stream):
+    """(pointer, bytes, keep-alive) of a workspace argument whose size the
+    library names through size(): None, "auto" or a tensor."""
+    if workspace is None:
+        return None, 0, None
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError("workspace must be None, 'auto' or a tensor")
+        n = size()
+        if n == 0:
+            return None, 0, None
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        return workspace.data_ptr(), n, workspace
+    _need(workspace, "workspace", device=dev)
+    workspace.record_stream(stream)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def gdn_scan_workspace_size(num_seqs, tokens, D, dtype, packed) -> int:
+    """Workspace bytes the scan calls can use (0: they would not use one)."""
+    code = _dtype_code(torch.empty(0, dtype=dtype)) if isinstance(dtype, torch.dtype) else dtype
+    return int(load_library().gdn_scan_workspace_size(num_seqs, tokens, D, code,
+                                                      int(bool(packed))))
+
+
+def _scan_forward(x, alpha, beta, cu, h0, out, final, want_final, prefix, interval, flags,
+                  workspace, stream):
+    lib = load_library()
+    code = _dtype_code(x)
+    dev, D = x.device, x.shape[-1]
+    packed = cu is not None
+    _need(x, "x")
+    _need(alpha, "alpha", x.dtype, x.shape, dev)
+    _opt(beta, "beta", x.dtype, x.shape, dev)
+    if packed:
+        _need(cu, "cu_seqlens", torch.int32, device=dev)
+        n, tokens = _dims(cu, "cu_seqlens", 1)[0] - 1, x.shape[0]
+    else:
+        n, tokens = x.shape[0], x.shape[1]
+    _opt(h0, "initial_state", torch.float32, (n, D), dev)
+    _opt(out, "out", x.dtype, x.shape, dev)
+    _opt(final, "final_state", torch.float32, (n, D), dev)
+    interval = int(interval)
+    if prefix is not None:
+        if interval < 1:
+            raise ValueError("prefix_interval must be >= 1 with prefix_states")
+        _need(prefix, "prefix_states", torch.float32,
+              (prefix_state_rows(n, tokens, interval, packed), D), dev)
+    on = _On(dev, stream)
+    with on as st:
+        if out is None:
+            out = torch.empty_like(x)
+        if final is None and want_final:
+            final = torch.empty((n, D), dtype=torch.float32, device=dev)
+        wp, wb, _keep = _scratch(
+            workspace, lambda: lib.gdn_scan_workspace_size(n, tokens, D, code, int(packed)), dev,
+            on.stream)
+        if packed:
+            rc = lib.gdn_scan_varlen_prefill(
+                x.data_ptr(), alpha.data_ptr(), _ptr(beta), cu.data_ptr(), n, tokens, _ptr(h0),
+                out.data_ptr(), _ptr(final), _ptr(prefix), interval, D, code, flags, wp, wb, st)
+        else:
+            rc = lib.gdn_scan_prefill(
+                x.data_ptr(), alpha.data_ptr(), _ptr(beta), _ptr(h0), out.data_ptr(), _ptr(final),
+                _ptr(prefix), interval, n, tokens, D, code, flags, wp, wb, st)
+    _check(rc)
+    return out, final
+
+
+def gdn_scan_prefill(x, alpha, beta=None, initial_state=None, *, out=None, final_state=None,
+                     want_final_state: bool = True, prefix_states=None, prefix_interval: int = 0,
+                     flags: int = 0, workspace="auto", stream=None):
+    """Gated linear recurrence h_t = alpha_t h_{t-1} + beta_t x_t per channel.
+    x, alpha, beta [B,T,D] of one dtype (beta None: 1 - alpha); initial_state
+    [B,D] fp32 or None. Returns (out [B,T,D], final_state [B,D] fp32).
+    prefix_states: optional fp32 [prefix_state_rows(B, T, interval, False), D]
+    receiving the state after every whole block of 64 * prefix_interval tokens
+    (gdn_scan_backward takes them with an interval of 1 or 2)."""
+    _dims(x, "x", 3)
+    return _scan_forward(x, alpha, beta, None, initial_state, out, final_state, want_final_state,
+                         prefix_states, prefix_interval, flags, workspace, stream)
+
+
+def gdn_scan_varlen_prefill(x, alpha, beta, cu_seqlens, initial_state=None, *, out=None,
+                            final_state=None, want_final_state: bool = True, prefix_states=None,
+                            prefix_interval: int = 0, flags: int = 0, workspace="auto",
+                            stream=None):
+    """gdn_scan_prefill over packed sequences: x, alpha, beta [total,D];
+    cu_seqlens int32 [N+1] on the device; states [N,D]."""
+    _dims(x, "x", 2)
+    _dims(cu_seqlens, "cu_seqlens", 1)
+    return _scan_forward(x, alpha, beta, cu_seqlens, initial_state, out, final_state,
+                         want_final_state, prefix_states, prefix_interval, flags, workspace,
+                         stream)
+
+
+def _scan_backward(dout, x, alpha, beta, cu, h0, prefix, interval, dfinal, dx, dalpha, dbeta,
+                   dinitial, want_dinitial, flags, workspace, stream):
+    lib = load_library()
+    code = _dtype_code(x)
+    dev, D = x.device, x.shape[-1]
+    packed = cu is not None
+    _need(x, "x")
+    _need(dout, "dout", x.dtype, x.shape, dev)
+    _need(alpha, "alpha", x.dtype, x.shape, dev)
+    _opt(beta, "beta", x.dtype, x.shape, dev)
+    if packed:
+        _need(cu, "cu_seqlens", torch.int32, device=dev)
+        n, tokens = _dims(cu, "cu_seqlens", 1)[0] - 1, x.shape[0]
+    else:
+        n, tokens = x.shape[0], x.shape[1]
+    _opt(h0, "initial_state", torch.float32, (n, D), dev)
+    _opt(dfinal, "dfinal", torch.float32, (n, D), dev)
+    _opt(dx, "dx", x.dtype, x.shape, dev)
+    _opt(dalpha, "dalpha", x.dtype, x.shape, dev)
+    _opt(dbeta, "dbeta", x.dtype, x.shape, dev)
+    _opt(dinitial, "dinitial", torch.float32, (n, D), dev)
+    if beta is None and dbeta is not None:
+        raise ValueError("dbeta must be None with tied gates (beta None)")
+    interval = int(interval)
+    if prefix is not None:
+        if interval < 1:
+            raise ValueError("prefix_interval must be >= 1 with prefix_states")
+        _need(prefix, "prefix_states", torch.float32,
+              (prefix_state_rows(n, tokens, interval, packed), D), dev)
+    elif tokens > SCAN_TILE:
+        raise ValueError(f"prefix_states are needed for more than {SCAN_TILE} tokens")
+    on = _On(dev, stream)
+    with on as st:
+        dx = torch.empty_like(x) if dx is None else dx
+        dalpha = torch.empty_like(x) if dalpha is None else dalpha
+        if beta is not None and dbeta is None:
+            dbeta = torch.empty_like(x)
+        if dinitial is None and want_dinitial:
+            dinitial = torch.empty((n, D), dtype=torch.float32, device=dev)
+        wp, wb, _keep = _scratch(
+            workspace, lambda: lib.gdn_scan_workspace_size(n, tokens, D, code, int(packed)), dev,
+            on.stream)
+        tail = (_ptr(prefix), interval, _ptr(dfinal), dx.data_ptr(), dalpha.data_ptr(),
+                _ptr(dbeta), _ptr(dinitial))
+        if packed:
+            rc = lib.gdn_scan_varlen_backward(
+                dout.data_ptr(), x.data_ptr(), alpha.data_ptr(), _ptr(beta), cu.data_ptr(), n,
+                tokens, _ptr(h0), *tail, D, code, flags, wp, wb, st)
+        else:
+            rc = lib.gdn_scan_backward(
+                dout.data_ptr(), x.data_ptr(), alpha.data_ptr(), _ptr(beta), _ptr(h0), *tail, n,
+                tokens, D, code, flags, wp, wb, st)
+    _check(rc)
+    return dx, dalpha, dbeta, dinitial
+
+
+def gdn_scan_backward(dout, x, alpha, beta=None, initial_state=None, *, prefix_states=None,
+                      prefix_interval: int = 0, dfinal=None, dx=None, dalpha=None, dbeta=None,
+                      dinitial=None, want_dinitial: bool = True, flags: int = 0,
+                      workspace="auto", stream=None):
+    """Gradients of gdn_scan_prefill: dout [B,T,D], dfinal [B,D] fp32 or None,
+    and the forward call's inputs, with the prefix states it wrote
+    (prefix_interval 1 or 2; None for T <= SCAN_TILE). Returns (dx, dalpha,
+    dbeta or None, dinitial [B,D] fp32 or None); with GDN_GATE_LOGITS dalpha
+    and dbeta are the logits' gradients."""
+    _dims(x, "x", 3)
+    return _scan_backward(dout, x, alpha, beta, None, initial_state, prefix_states,
+                          prefix_interval, dfinal, dx, dalpha, dbeta, dinitial, want_dinitial,
+                          flags, workspace, stream)
+
+
+def gdn_scan_varlen_backward(dout, x, alpha, beta, cu_seqlens, initial_state=None, *,
+                             prefix_states=None, prefix_interval: int = 0, dfinal=None, dx=None,
+                             dalpha=None, dbeta=None, dinitial=None, want_dinitial: bool = True,
+                             flags: int = 0, workspace="auto", stream=None):
+    """Gradients of gdn_scan_varlen_prefill: tensors [total,D], states [N,D]."""
+    _dims(x, "x", 2)
+    _dims(cu_seqlens, "cu_seqlens", 1)
+    return _scan_backward(dout, x, alpha, beta, cu_seqlens, initial_state, prefix_states,
+                          prefix_interval, dfinal, dx, dalpha, dbeta, dinitial, want_dinitial,
+                          flags, workspace, stream)
+
+
+def gdn_scan_decode(x, alpha, beta, state_pool, src_slot, dst_slot, *, out=None, flags: int = 0,
+                    stream=None):
+    """K tokens of the gated linear recurrence per sequence against a pool of
+    state slots. x, alpha, beta [B,K,D] (beta None: 1 - alpha); state_pool
+    [num_slots,D] fp32; src_slot, dst_slot int32 [B] on the device (negative
+    src = zero state, negative dst = not written). Returns out [B,K,D]."""
+    lib = load_library()
+    B, K, D = _dims(x, "x", 3)
+    code, dev = _dtype_code(x), x.device
+    _need(x, "x")
+    _need(alpha, "alpha", x.dtype, x.shape, dev)
+    _opt(beta, "beta", x.dtype, x.shape, dev)
+    num_slots, _ = _dims(state_pool, "state_pool", 2)
+    _need(state_pool, "state_pool", torch.float32, (num_slots, D), dev)
+    _need(src_slot, "src_slot", torch.int32, (B,), dev)
+    _need(dst_slot, "dst_slot", torch.int32, (B,), dev)
+    _opt(out, "out", x.dtype, x.shape, dev)
+    with _On(dev, stream) as st:
+        if out is None:
+            out = torch.empty_like(x)
+        rc = lib.gdn_scan_decode(x.data_ptr(), alpha.data_ptr(), _ptr(beta),
+                                 state_pool.data_ptr(), num_slots, src_slot.data_ptr(),
+                                 dst_slot.data_ptr(), out.data_ptr(), B, K, D, code, flags, st)
+    _check(rc)
+    return out
+
+
+def gdn_rms_norm(x, weight, residual=None, *, eps: float = 1e-6, group: int = 0,
+                 want_out: bool = True, want_out8: bool = False, want_residual: bool = True,
+                 out=None, out8=None, scales=None, residual_out=None, stream=None):
+    """RMS norm over the last dimension of x (any leading dimensions), with the
+    residual's addition and an output in 8 bits. x, residual, weight [D] of one
+    dtype. Returns (out, out8, scales, residual_out), None where not wanted:
+    out8 is torch.float8_e4m3fn with fp32 scales, one per row (group 0, shape
+    [..., 1]) or per 128 columns (group 128, [..., ceil(D / 128)]);
+    residual_out is x + residual (pass residual itself to update it in place)."""
+    lib = load_library()
+    code, dev = _dtype_code(x), x.device
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError(f"x must have a last dimension of at least 1, got {tuple(x.shape)}")
+    D = x.shape[-1]
+    rows = x.numel() // D
+    _need(x, "x")
+    _need(weight, "weight", x.dtype, (D,), dev)
+    _opt(residual, "residual", x.dtype, x.shape, dev)
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if group not in (0, 128):
+        raise ValueError(f"group must be 0 (one scale per row) or 128, got {group}")
+    _opt(out, "out", x.dtype, x.shape, dev)
+    _opt(out8, "out8", torch.float8_e4m3fn, x.shape, dev)
+    sshape = (*x.shape[:-1], 1 if group == 0 else -(-D // 128))
+    _opt(scales, "scales", torch.float32, sshape, dev)
+    _opt(residual_out, "residual_out", x.dtype, x.shape, dev)
+    want_out8 = want_out8 or out8 is not None or scales is not None
+    with _On(dev, stream) as st:
+        if out is None and want_out:
+            out = torch.empty_like(x)
+        if want_out8:
+            out8 = torch.empty_like(x, dtype=torch.float8_e4m3fn) if out8 is None else out8
+            if scales is None:
+                scales = torch.empty(sshape, dtype=torch.float32, device=dev)
+        if residual is not None and residual_out is None and want_residual:
+            residual_out = torch.empty_like(x)
+        rc = lib.gdn_rms_norm(x.data_ptr(), _ptr(residual), weight.data_ptr(),
+                              _ptr(residual_out), _ptr(out), _ptr(out8), _ptr(scales), group,
+                              rows, D, code, eps, st)
+    _check(rc)
+    return out, out8, scales, residual_out
+
+
+def gdn_rms_norm_backward(dout, r, weight, dresidual=None, *, eps: float = 1e-6,
+                          want_dweight: bool = True, dx=None, dweight=None, workspace="auto",
+                          stream=None):
+    """Gradients of gdn_rms_norm at the row sums r (residual_out, or x without
+    a residual): dout, r [..., D]; dresidual, the gradient that arrives at
+    residual_out, or None. Returns (dx, dweight fp32 [D] or None); dx is the
+    gradient of x and of residual alike and may be dresidual itself."""
+    lib = load_library()
+    code, dev = _dtype_code(r), r.device
+    if r.dim() < 1 or r.shape[-1] < 1:
+        raise ValueError(f"r must have a last dimension of at least 1, got {tuple(r.shape)}")
+    D = r.shape[-1]
+    rows = r.numel() // D
+    _need(r, "r")
+    _need(dout, "dout", r.dtype, r.shape, dev)
+    _need(weight, "weight", r.dtype, (D,), dev)
+    _opt(dresidual, "dresidual", r.dtype, r.shape, dev)
+    _opt(dx, "dx", r.dtype, r.shape, dev)
+    _opt(dweight, "dweight", torch.float32, (D,), dev)
+    on = _On(dev, stream)
+    with on as st:
+        if dx is None:
+            dx = torch.empty_like(r)
+        if dweight is None and want_dweight:
+            dweight = torch.empty(D, dtype=torch.float32, device=dev)
+        wp, wb, _keep = None, 0, None
+        if dweight is not None:
+            wp, wb, _keep = _scratch(workspace, lambda: lib.gdn_rms_norm_workspace_size(rows, D),
+                                     dev, on.stream)
+        rc = lib.gdn_rms_norm_backward(dout.data_ptr(), r.data_ptr(), weight.data_ptr(),
+                                       _ptr(dresidual), dx.data_ptr(), _ptr(dweight), rows, D,
+                                       code, eps, wp, wb, st)
+    _check(rc)
+    return dx, dweight
+
+
+def gdn_beam_select(logits, scores, *, finished=None, eos: int = -1, beam_slots=None,
+                    new_scores=None, tokens=None, parents=None, new_finished=None,
+                    src_slots=None, workspace="auto", stream=None):
+    """Beam search's selection. logits [B,W,V] (bf16 or fp32); scores [B,W]
+    fp32, the beams' summed log-probabilities; finished uint8 [B,W] or None;
+    eos the end token (-1: none); beam_slots int32 [B,W] or None, the beams'
+    state slots. Returns (new_scores, tokens, parents, new_finished, src_slots),
+    all [B,W], best first: parents are beam indices within the batch item,
+    src_slots the parents' slots (the src_slot of the next decode call, or
+    gdn_gather_states' index). new_finished is None without eos, src_slots
+    without beam_slots."""
+    lib = load_library()
+    B, W, V = _dims(logits, "logits", 3)
+    code, dev = _dtype_code(logits), logits.device
+    _need(logits, "logits")
+    shape = (B, W)
+    _need(scores, "scores", torch.float32, shape, dev)
+    _opt(finished, "finished", torch.uint8, shape, dev)
+    _opt(beam_slots, "beam_slots", torch.int32, shape, dev)
+    for t, name, dtype in ((new_scores, "new_scores", torch.float32),
+                           (tokens, "tokens", torch.int32), (parents, "parents", torch.int32),
+                           (new_finished, "new_finished", torch.uint8),
+                           (src_slots, "src_slots", torch.int32)):
+        if t is not None:
+            _need(t, name, dtype, shape, dev)
+    if finished is not None and eos < 0:
+        raise ValueError("finished needs eos")
+    on = _On(dev, stream)
+    with on as st:
+        if new_scores is None:
+            new_scores = torch.empty(shape, dtype=torch.float32, device=dev)
+        if tokens is None:
+            tokens = torch.empty(shape, dtype=torch.int32, device=dev)
+        if parents is None:
+            parents = torch.empty(shape, dtype=torch.int32, device=dev)
+        if new_finished is None and eos >= 0:
+            new_finished = torch.empty(shape, dtype=torch.uint8, device=dev)
+        if src_slots is None and beam_slots is not None:
+            src_slots = torch.empty(shape, dtype=torch.int32, device=dev)
+        wp, wb, _keep = _scratch(workspace, lambda: lib.gdn_beam_workspace_size(B, W, V, code),
+                                 dev, on.stream)
+        rc = lib.gdn_beam_select(logits.data_ptr(), scores.data_ptr(), _ptr(finished),
+                                 _ptr(beam_slots), new_scores.data_ptr(), tokens.data_ptr(),
+                                 parents.data_ptr(), _ptr(new_finished), _ptr(src_slots), B, W, V,
+                                 eos, code, wp, wb, st)
+    _check(rc)
+    return new_scores, tokens, parents, new_finished, src_slots
+
+
+def gdn_gather_states(states, index, *, out=None, stream=None):
+    """Rows of a state buffer in a new order: out[i] = states[index[i]], any
+    dtype, rows of a multiple of 16 bytes. index int32 [R] on the device (negative:
+    zeros; past the end: bytes of 0xff). out must not overlap states."""
+    lib = load_library()
+    if not isinstance(states, torch.Tensor) or states.dim() < 1:
+        raise ValueError("states must be a tensor with a first dimension of rows")
+    dev = states.device
+    _need(states, "states")
+    R = _dims(index, "index", 1)[0]
+    _need(index, "index", torch.int32, device=dev)
+    shape = (R, *states.shape[1:])
+    row_bytes = math.prod(states.shape[1:]) * states.element_size()
+    _opt(out, "out", states.dtype, shape, dev)
+    with _On(dev, stream) as st:
+        if out is None:
+            out = torch.empty(shape, dtype=states.dtype, device=dev)
+        rc = lib.gdn_gather_states(states.data_ptr(), states.shape[0], index.data_ptr(),
+                                   out.data_ptr(), R, row_bytes, st)
+    _check(rc)
+    return out
 
 
 def gdn_version() -> int:

@@ -13,17 +13,17 @@
 
 #include "../../include/gdn.h"
 #include "gdn_launch.hpp"
+#include "gdn_ops_launch.hpp"
 #include "gdn_validate.hpp"
 
 namespace {
+thread_local char g_detail[256];
+}
+
+// Shared with the other entry points (gdn_ops_api.hip).
+namespace gdn {
 
 using namespace gdn::val;
-
-thread_local char g_detail[256];
-
-constexpr uint32_t kKnownFlags = GDN_QK_L2NORM | GDN_GATE_LOGITS;
-static_assert(GDN_QK_L2NORM == gdn::kQkL2Norm && GDN_GATE_LOGITS == gdn::kGateLogits,
-              "flag values of the ABI and the kernels");
 
 gdn_status_t hip_fail(hipError_t e, const char *where) {
     snprintf(g_detail, sizeof g_detail, "HIP error in %s: %s (%d)", where, hipGetErrorString(e),
@@ -59,6 +59,20 @@ gdn_status_t debug_cu_seqlens(const int32_t *cu, int32_t N, int64_t total_T, hip
     if (e != hipSuccess) return hip_fail(e, "GDN_DEBUG copy of cu_seqlens");
     return check_cu_seqlens(h.data(), N, total_T);
 }
+
+}  // namespace gdn
+
+namespace {
+
+using namespace gdn::val;
+using gdn::debug_checks;
+using gdn::debug_cu_seqlens;
+using gdn::device_cus;
+using gdn::hip_fail;
+
+constexpr uint32_t kKnownFlags = GDN_QK_L2NORM | GDN_GATE_LOGITS;
+static_assert(GDN_QK_L2NORM == gdn::kQkL2Norm && GDN_GATE_LOGITS == gdn::kGateLogits,
+              "flag values of the ABI and the kernels");
 
 gdn_status_t debug_clear_status(void *ws, hipStream_t stream) {
     const hipError_t e = hipMemsetAsync(ws, 0, gdn::kWsStatusBytes, stream);
@@ -132,16 +146,17 @@ const char *gdn_status_string(gdn_status_t s) {
     case GDN_ERR_NULL_POINTER: return "a required pointer is NULL";
     case GDN_ERR_BAD_SHAPE: return "a size is out of range or inconsistent";
     case GDN_ERR_UNSUPPORTED:
-        return "unsupported dtype or head dimension (Dk == Dv in {64, 128}), or a shape whose "
-               "scratch exceeds the static 64 MiB of gdn_prefill_chunked_noalloc";
-    case GDN_ERR_MISALIGNED: return "a pointer is not 16-byte aligned";
+        return "unsupported dtype, flag or head dimension (Dk == Dv in {64, 128}), a shape whose "
+               "scratch exceeds the static 64 MiB of gdn_prefill_chunked_noalloc, or a width, "
+               "group, interval or beam count the library has no kernel for";
+    case GDN_ERR_MISALIGNED: return "a pointer is not 16-byte aligned (index arrays: 4-byte)";
     case GDN_ERR_ALIAS: return "forbidden overlap between buffers";
     case GDN_ERR_HIP: return g_detail[0] ? g_detail : "HIP runtime error";
     }
     return "unknown status";
 }
 
-int32_t gdn_version(void) { return 500; }
+int32_t gdn_version(void) { return 600; }
 
 size_t gdn_prefill_workspace_size(int32_t num_seqs, int64_t tokens, int32_t Hk, int32_t Hv,
                                   int32_t Dk, int32_t Dv, gdn_dtype_t dtype, int32_t packed) {

@@ -1,0 +1,413 @@
+// gdn_norm.hip -- root-mean-square norm with the residual's addition and an
+// output in 8 bits with scales (gfx950), and its gradients.
+//
+//   r = x + residual,  s = 1 / sqrt(mean(r^2) + eps),  y = r s w
+//   out8 = e4m3(y / scale),  scale = max |y| / 448 per row or 128 columns
+//   dr = s w dy - r s^3 mean(w dy r) + dresidual,  dw = sum over rows of dy r s
+//
+// A handful of operations per element: bound by HBM traffic, each row read
+// once and held in registers between the sum of squares and the outputs.
+//
+// Mapping: a thread holds chunks of 8 neighbouring columns (16 bytes of bf16).
+// 16 threads share a row of up to 128 columns, a wave one of up to 512, and a
+// workgroup a wider one, so that a 128-column group is always 16 neighbouring
+// lanes and its maximum one DPP row reduction.
+#include "gdn_device.hpp"
+#include "gdn_ops_launch.hpp"
+
+namespace gdn {
+
+namespace {
+
+constexpr float kE4m3Max = 448.f;
+constexpr float kScaleFloor = 0x1p-100f;  // groups of zeros keep a finite scale and its inverse
+
+__device__ __forceinline__ float row16_max(float x) {
+    x = fmaxf(x, GDN_DPP(x, 0xB1));
+    x = fmaxf(x, GDN_DPP(x, 0x4E));
+    x = fmaxf(x, GDN_DPP(x, 0x141));
+    x = fmaxf(x, GDN_DPP(x, 0x140));
+    return x;
+}
+
+struct SumOp {
+    static __device__ __forceinline__ float row16(float x) { return row16_sum(x); }
+    static __device__ __forceinline__ float two(float a, float b) { return a + b; }
+};
+struct MaxOp {
+    static __device__ __forceinline__ float row16(float x) { return row16_max(x); }
+    static __device__ __forceinline__ float two(float a, float b) { return fmaxf(a, b); }
+};
+
+// Reduction over the threads that share a row: 16 lanes, a wave, or the
+// workgroup (TPR 0; `red` holds one value per wave and is free for the next
+// reduction only after another barrier).
+template <int TPR, typename Op> __device__ __forceinline__ float row_reduce(float x, float *red) {
+    x = Op::row16(x);
+    if constexpr (TPR != 16) {
+        x = Op::two(x, __shfl_xor(x, 16));
+        x = Op::two(x, __shfl_xor(x, 32));
+    }
+    if constexpr (TPR == 0) {
+        const int waves = blockDim.x >> 6;
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
+        __syncthreads();
+        x = red[0];
+        for (int w = 1; w < waves; ++w) x = Op::two(x, red[w]);
+    }
+    return x;
+}
+
+// 8 elements at p: one or two 16-byte accesses, or (rows that do not start on
+// 16 bytes) element by element up to `left` of them.
+template <typename DT, bool VEC>
+__device__ __forceinline__ void load8(const DT *p, int left, float (&x)[8]) {
+    if constexpr (VEC) {
+        if constexpr (sizeof(DT) == 2) {
+            const bf16x8 v = *reinterpret_cast<const bf16x8 *>(p);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = (float)v[e];
+        } else {
+            const f32x4 a = reinterpret_cast<const f32x4 *>(p)[0];
+            const f32x4 b = reinterpret_cast<const f32x4 *>(p)[1];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[e] = a[e];
+                x[e + 4] = b[e];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = e < left ? to_f32(p[e]) : 0.f;
+    }
+}
+template <typename DT, bool VEC>
+__device__ __forceinline__ void store8(DT *p, int left, const float (&x)[8]) {
+    if constexpr (VEC) {
+        if constexpr (sizeof(DT) == 2) {
+            bf16x8 v;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = (__bf16)x[e];
+            *reinterpret_cast<bf16x8 *>(p) = v;
+        } else {
+            reinterpret_cast<f32x4 *>(p)[0] = f32x4{x[0], x[1], x[2], x[3]};
+            reinterpret_cast<f32x4 *>(p)[1] = f32x4{x[4], x[5], x[6], x[7]};
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < left) p[e] = from_f32<DT>(x[e]);
+    }
+}
+
+// 8 values in OCP e4m3, rounded to nearest even.
+template <bool VEC>
+__device__ __forceinline__ void store8_e4m3(uint8_t *p, int left, const float (&x)[8]) {
+    int lo = 0, hi = 0;
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], lo, false);
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], lo, true);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[4], x[5], hi, false);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[6], x[7], hi, true);
+    if constexpr (VEC) {
+        *reinterpret_cast<u32x2 *>(p) = u32x2{(uint32_t)lo, (uint32_t)hi};
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < left) p[e] = (uint8_t)((uint32_t)(e < 4 ? lo : hi) >> (8 * (e & 3)));
+    }
+}
+
+// Threads that share a row and the row of this thread.
+template <int TPR> __device__ __forceinline__ int row_threads() {
+    return TPR == 0 ? (int)blockDim.x : TPR;
+}
+
+template <typename DT, bool VEC, int TPR, int CH>
+__global__ __launch_bounds__(1024) void norm_kernel(NormParams p) {
+    __shared__ float s_red[2][16];
+    const int tpr = row_threads<TPR>();
+    const int j = TPR == 0 ? threadIdx.x : threadIdx.x % tpr;
+    const int64_t row = TPR == 0 ? blockIdx.x
+                                 : (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
+    const int D = p.D;
+    const bool live = row < p.rows;  // no early exit: the lanes of a wave reduce together
+    const int64_t at = row * D;
+    float r[CH][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+        const int c = (k * tpr + j) * 8, left = live ? D - c : 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[k][e] = 0.f;
+        if (left > 0) {
+            load8<DT, VEC>(reinterpret_cast<const DT *>(p.x) + at + c, left, r[k]);
+            if (p.res) {
+                float q[8];
+                load8<DT, VEC>(reinterpret_cast<const DT *>(p.res) + at + c, left, q);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) r[k][e] += q[e];
+                if (p.res_out)
+                    store8<DT, VEC>(reinterpret_cast<DT *>(p.res_out) + at + c, left, r[k]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(r[k][e], r[k][e], ss);
+    }
+    ss = row_reduce<TPR, SumOp>(ss, s_red[0]);
+    const float s = 1.f / sqrtf(ss / (float)D + p.eps);
+    float most = 0.f;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+        const int c = (k * tpr + j) * 8, left = live ? D - c : 0;
+        if (left > 0) {
+            float w[8];
+            load8<DT, VEC>(reinterpret_cast<const DT *>(p.w) + c, left, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r[k][e] = r[k][e] * s * w[e];
+            if (p.out) store8<DT, VEC>(reinterpret_cast<DT *>(p.out) + at + c, left, r[k]);
+        }
+        if (!p.out8) continue;
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(r[k][e]));
+        if (p.group == 0) {
+            most = fmaxf(most, m);
+        } else {  // 128 columns: the 16 lanes of a DPP row
+            m = fmaxf(row16_max(m) / kE4m3Max, kScaleFloor);
+            const float inv = 1.f / m;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r[k][e] *= inv;
+            if (left > 0) {
+                store8_e4m3<VEC>(p.out8 + at + c, left, r[k]);
+                if ((j & 15) == 0) p.scales[row * ((D + 127) / 128) + c / 128] = m;
+            }
+        }
+    }
+    if (p.out8 && p.group == 0) {
+        most = row_reduce<TPR, MaxOp>(most, s_red[1]);
+        const float scale = fmaxf(most / kE4m3Max, kScaleFloor), inv = 1.f / scale;
+        if (live && j == 0) p.scales[row] = scale;
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            const int c = (k * tpr + j) * 8, left = live ? D - c : 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r[k][e] *= inv;
+            if (left > 0) store8_e4m3<VEC>(p.out8 + at + c, left, r[k]);
+        }
+    }
+}
+
+// dx per row, and each workgroup's share of dw: a thread keeps the sums of its
+// columns over the workgroup's rows, the workgroup joins the threads that hold
+// the same columns, and norm_dweight_kernel joins the workgroups in order.
+template <typename DT, bool VEC, int TPR, int CH>
+__global__ __launch_bounds__(1024) void norm_backward_kernel(NormBackwardParams p) {
+    __shared__ float s_red[2][16];
+    __shared__ float s_dw[TPR == 0 ? 1 : 256 * 8 * CH];
+    const int tpr = row_threads<TPR>();
+    const int j = TPR == 0 ? threadIdx.x : threadIdx.x % tpr;
+    const int per = TPR == 0 ? 1 : blockDim.x / tpr;  // rows side by side
+    const int D = p.D;
+    float w[CH][8], dw[CH][8];
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+        const int c = (k * tpr + j) * 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            w[k][e] = 0.f;
+            dw[k][e] = 0.f;
+        }
+        if (c < D) load8<DT, VEC>(reinterpret_cast<const DT *>(p.w) + c, D - c, w[k]);
+    }
+    int turn = 0;
+    for (int64_t row0 = (int64_t)blockIdx.x * per; row0 < p.rows;
+         row0 += (int64_t)gridDim.x * per, turn ^= 1) {
+        const int64_t row = row0 + (TPR == 0 ? 0 : threadIdx.x / tpr);
+        const bool live = row < p.rows;
+        const int64_t at = row * D;
+        float r[CH][8], dy[CH][8];
+        float ss = 0.f, dot = 0.f;
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            const int c = (k * tpr + j) * 8, left = live ? D - c : 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                r[k][e] = 0.f;
+                dy[k][e] = 0.f;
+            }
+            if (left > 0) {
+                load8<DT, VEC>(reinterpret_cast<const DT *>(p.r) + at + c, left, r[k]);
+                load8<DT, VEC>(reinterpret_cast<const DT *>(p.dout) + at + c, left, dy[k]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                ss = fmaf(r[k][e], r[k][e], ss);
+                dot = fmaf(w[k][e] * dy[k][e], r[k][e], dot);
+            }
+        }
+        if constexpr (TPR == 0) {  // both sums in one exchange
+            __shared__ float s_two[2][2][16];
+            const int waves = blockDim.x >> 6, wave = threadIdx.x >> 6;
+            ss = row_reduce<64, SumOp>(ss, nullptr);
+            dot = row_reduce<64, SumOp>(dot, nullptr);
+            if ((threadIdx.x & 63) == 0) {
+                s_two[turn][0][wave] = ss;
+                s_two[turn][1][wave] = dot;
+            }
+            __syncthreads();  // the other turn's values were read before this barrier
+            ss = s_two[turn][0][0];
+            dot = s_two[turn][1][0];
+            for (int i = 1; i < waves; ++i) {
+                ss += s_two[turn][0][i];
+                dot += s_two[turn][1][i];
+            }
+        } else {
+            ss = row_reduce<TPR, SumOp>(ss, s_red[0]);
+            dot = row_reduce<TPR, SumOp>(dot, s_red[1]);
+        }
+        const float s = 1.f / sqrtf(ss / (float)D + p.eps);
+        const float m = s * s * s * (dot / (float)D);
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            const int c = (k * tpr + j) * 8, left = live ? D - c : 0;
+            if (left <= 0) continue;
+            float dx[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dx[e] = 0.f;
+            if (p.dres) load8<DT, VEC>(reinterpret_cast<const DT *>(p.dres) + at + c, left, dx);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                dx[e] += s * w[k][e] * dy[k][e] - r[k][e] * m;
+                dw[k][e] = fmaf(dy[k][e], r[k][e] * s, dw[k][e]);
+            }
+            store8<DT, VEC>(reinterpret_cast<DT *>(p.dx) + at + c, left, dx);
+        }
+    }
+    if (!p.dw) return;
+    float *part = p.partial + (int64_t)blockIdx.x * D;
+    if constexpr (TPR == 0) {
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            const int c = (k * tpr + j) * 8;
+            if (c < D) store8<float, VEC>(part + c, D - c, dw[k]);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < CH; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s_dw[(threadIdx.x * CH + k) * 8 + e] = dw[k][e];
+        __syncthreads();
+        if ((int)threadIdx.x < tpr) {
+            for (int i = 1; i < per; ++i)
+#pragma unroll
+                for (int k = 0; k < CH; ++k)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        dw[k][e] += s_dw[((threadIdx.x + i * tpr) * CH + k) * 8 + e];
+#pragma unroll
+            for (int k = 0; k < CH; ++k) {
+                const int c = (k * tpr + j) * 8;
+                if (c < D) store8<float, VEC>(part + c, D - c, dw[k]);
+            }
+        }
+    }
+}
+
+// dw[c] = sum over the partials, 16 threads per column and a fixed order.
+__global__ __launch_bounds__(1024) void norm_dweight_kernel(const float *partial, int count,
+                                                            float *dw, int D) {
+    __shared__ float s_sum[16][64];
+    const int lane = threadIdx.x & 63, part = threadIdx.x >> 6;
+    const int c = blockIdx.x * 64 + lane;
+    float sum = 0.f;
+    if (c < D)
+        for (int i = part; i < count; i += 16) sum += partial[(int64_t)i * D + c];
+    s_sum[part][lane] = sum;
+    __syncthreads();
+    if (part == 0 && c < D) {
+        for (int i = 1; i < 16; ++i) sum += s_sum[i][lane];
+        dw[c] = sum;
+    }
+}
+
+// How a row is shared out: threads per row (16, 64 or a workgroup), chunks of
+// 8 columns per thread, threads per workgroup and rows per workgroup.
+struct NormPlan {
+    int tpr, ch, threads, per;
+};
+
+NormPlan plan_norm(int32_t D) {
+    const int chunks = (D + 7) / 8;
+    if (chunks <= 16) return {16, 1, 256, 16};
+    if (chunks <= 64) return {64, 1, 256, 4};
+    const int ch = chunks > 1024 ? 2 : 1;
+    const int threads = ((chunks + ch - 1) / ch + 63) / 64 * 64;
+    return {0, ch, threads, 1};
+}
+
+template <typename F> hipError_t with_norm_types(int dtype, int32_t D, const NormPlan &n, F &&f) {
+    const bool vec = D % 8 == 0;
+#define GDN_NORM_CASE(DT, VEC)                                                   \
+    do {                                                                         \
+        if (n.tpr == 16) return f.template run<DT, VEC, 16, 1>(n);               \
+        if (n.tpr == 64) return f.template run<DT, VEC, 64, 1>(n);               \
+        if (n.ch == 1) return f.template run<DT, VEC, 0, 1>(n);                  \
+        return f.template run<DT, VEC, 0, 2>(n);                                 \
+    } while (0)
+    if (dtype == 1) {
+        if (vec) GDN_NORM_CASE(__bf16, true);
+        GDN_NORM_CASE(__bf16, false);
+    }
+    if (vec) GDN_NORM_CASE(float, true);
+    GDN_NORM_CASE(float, false);
+#undef GDN_NORM_CASE
+}
+
+struct RunNorm {
+    const NormParams &p;
+    hipStream_t stream;
+    template <typename DT, bool VEC, int TPR, int CH> hipError_t run(const NormPlan &n) const {
+        hipLaunchKernelGGL((norm_kernel<DT, VEC, TPR, CH>),
+                           dim3((unsigned)((p.rows + n.per - 1) / n.per)), dim3(n.threads), 0,
+                           stream, p);
+        return hipGetLastError();
+    }
+};
+
+struct RunNormBackward {
+    const NormBackwardParams &p;
+    hipStream_t stream;
+    template <typename DT, bool VEC, int TPR, int CH> hipError_t run(const NormPlan &n) const {
+        hipLaunchKernelGGL((norm_backward_kernel<DT, VEC, TPR, CH>),
+                           dim3((unsigned)norm_partials(p.rows, p.D)), dim3(n.threads), 0,
+                           stream, p);
+        return hipGetLastError();
+    }
+};
+
+}  // namespace
+
+hipError_t launch_norm(const NormParams &p, int dtype, hipStream_t stream) {
+    return with_norm_types(dtype, p.D, plan_norm(p.D), RunNorm{p, stream});
+}
+
+// Workgroups of the backward pass, each with a row of partial sums.
+int norm_partials(int64_t rows, int32_t D) {
+    const int64_t per = plan_norm(D).per, wgs = (rows + per - 1) / per;
+    return (int)(wgs < 512 ? wgs : 512);
+}
+
+hipError_t launch_norm_backward(const NormBackwardParams &p, int dtype, hipStream_t stream) {
+    const int count = norm_partials(p.rows, p.D);
+    if (count > 0) {
+        const hipError_t e =
+            with_norm_types(dtype, p.D, plan_norm(p.D), RunNormBackward{p, stream});
+        if (e != hipSuccess) return e;
+    }
+    if (p.dw)
+        hipLaunchKernelGGL(norm_dweight_kernel, dim3((unsigned)((p.D + 63) / 64)), dim3(1024), 0,
+                           stream, p.partial, count, p.dw, p.D);
+    return hipGetLastError();
+}
+
+}  // namespace gdn

@@ -1,0 +1,140 @@
+// gdn_scan.hpp -- device-side pieces of the gated linear recurrence kernels:
+// vector access, the gates, and the tile shape.
+#pragma once
+#include "gdn_device.hpp"
+#include "gdn_ops_launch.hpp"
+
+namespace gdn {
+
+// VEC neighbouring elements in their storage type: one access of their size.
+template <typename DT, int VEC> struct alignas(sizeof(DT) * VEC) Raw {
+    DT v[VEC];
+    __device__ __forceinline__ float operator[](int e) const { return to_f32(v[e]); }
+    __device__ __forceinline__ void set(int e, float x) { v[e] = from_f32<DT>(x); }
+};
+// VEC elements `bytes` behind base: 32-bit byte offsets within a tile
+// (kMaxScanWidth keeps them in range), so that the tile's start stays in scalar
+// registers.
+template <int VEC, typename DT>
+__device__ __forceinline__ Raw<DT, VEC> load_raw(const DT *base, uint32_t bytes) {
+    return *reinterpret_cast<const Raw<DT, VEC> *>(reinterpret_cast<const char *>(base) + bytes);
+}
+template <typename DT, int VEC>
+__device__ __forceinline__ void store_raw(DT *base, uint32_t bytes, const Raw<DT, VEC> &x) {
+    *reinterpret_cast<Raw<DT, VEC> *>(reinterpret_cast<char *>(base) + bytes) = x;
+}
+template <typename DT> __device__ __forceinline__ const DT *as(const void *p, int64_t at) {
+    return static_cast<const DT *>(p) + at;
+}
+template <typename DT> __device__ __forceinline__ DT *as(void *p, int64_t at) {
+    return static_cast<DT *>(p) + at;
+}
+
+// Makes the compiler forget what it derived from x: gates are computed anew
+// behind this instead of being kept in registers across a barrier.
+template <typename DT, int VEC> __device__ __forceinline__ void forget(Raw<DT, VEC> &x) {
+    if constexpr (sizeof(x) % 4 == 0) {
+        uint32_t w[sizeof(x) / 4];
+        __builtin_memcpy(w, &x, sizeof(x));
+#pragma unroll
+        for (size_t i = 0; i < sizeof(x) / 4; ++i) asm volatile("" : "+v"(w[i]));
+        __builtin_memcpy(&x, w, sizeof(x));
+    } else {
+        uint32_t w = __builtin_bit_cast(uint16_t, x.v[0]);
+        asm volatile("" : "+v"(w));
+        x.v[0] = __builtin_bit_cast(DT, (uint16_t)w);
+    }
+}
+
+template <typename DT, int VEC, int R>
+__device__ __forceinline__ void forget_all(Raw<DT, VEC> (&x)[R]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) forget(x[r]);
+}
+
+// e^z for z in [-110, 80] (held there outside), the product z log2(e) carried in two terms (Cody and
+// Waite's reduction in base 2): a plain product would be off by |z| 2^-24, and
+// the small gates 1 - alpha inherit that error whole.
+__device__ __forceinline__ float exp_two_term(float z) {
+    constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0bep-26f, kLn2 = 0x1.62e430p-1f;
+    z = z > 80.f ? 80.f : z;  // keeps 1 + e^z finite; a NaN stays one
+    z = z < -110.f ? -110.f : z;  // e^z is 0 there, and the product stays finite
+    const float t = z * kLog2e;
+    const float low = fmaf(z, kLog2eLow, fmaf(z, kLog2e, -t));
+    const float e = __builtin_amdgcn_exp2f(t);
+    return fmaf(e, low * kLn2, e);
+}
+
+// s = 1 / (1 + e^z) and its complement e^z / (1 + e^z), each to about one
+// unit in its own last place: the reciprocal takes one Newton step, because
+// the errors of an alpha near 1 add up over its memory of 1 / (1 - alpha)
+// tokens.
+__device__ __forceinline__ void sigmoid_pair(float z, float &s, float &c) {
+    const float e = exp_two_term(z);
+    const float d = 1.f + e;
+    float r = __builtin_amdgcn_rcpf(d);
+    r = fmaf(r, fmaf(-d, r, 1.f), r);
+    s = r;
+    c = e * r;
+}
+
+// Gates of one element from what the caller passes: the decay, its complement
+// and the write strength (tied: the complement).
+template <bool TIED, bool LOGITS>
+__device__ __forceinline__ void gates(float a, float b, float &alpha, float &keep, float &beta) {
+    if constexpr (LOGITS) {
+        sigmoid_pair(a, alpha, keep);
+        if constexpr (!TIED) {
+            float unused;
+            sigmoid_pair(-b, beta, unused);
+        }
+    } else {
+        alpha = a;
+        keep = 1.f - a;
+        beta = b;
+    }
+    if constexpr (TIED) beta = keep;
+}
+
+// A tile is kRows tokens by kCols channels on kThreads threads. kLanes
+// neighbouring lanes hold one token's kCols channels, VEC each; the kGroups
+// groups of them hold kPer consecutive tokens each.
+template <typename DT, int VEC> struct ScanShape {
+    static constexpr int kThreads = VEC == 1 ? 1024 : 512;
+    static constexpr int kRows = GDN_SCAN_TILE;
+    static constexpr int kLanes = VEC == 1 ? 64 : 16;
+    static constexpr int kCols = kLanes * VEC;
+    static constexpr int kGroups = kThreads / kLanes;
+    static constexpr int kPer = kRows / kGroups;
+    static_assert(kGroups * kPer == kRows, "tile shape");
+};
+
+// First token and length of sequence n, clamped into the batch.
+__device__ __forceinline__ void scan_bounds(const ScanParams &p, int n, int64_t &base,
+                                            int64_t &len) {
+    if (p.cu) {
+        int64_t lo = p.cu[n], hi = p.cu[n + 1];
+        lo = lo < 0 ? 0 : (lo > p.total ? p.total : lo);
+        hi = hi < lo ? lo : (hi > p.total ? p.total : hi);
+        base = lo;
+        len = hi - lo;
+    } else {
+        base = (int64_t)n * p.T;
+        len = p.T;
+    }
+}
+
+// Row of the prefix states of sequence n's block 0.
+__device__ __forceinline__ int64_t scan_prefix_row(const ScanParams &p, int n, int64_t base) {
+    return p.cu ? base / p.prefix_len + n : (int64_t)n * (p.T / p.prefix_len);
+}
+
+// Block that ends at token t, a multiple of 64 (the blocks are 64 m tokens):
+// its index, or -1 when no block ends there.
+__device__ __forceinline__ int64_t scan_block_ending(const ScanParams &p, int64_t t) {
+    const uint32_t units = (uint32_t)(t >> 6), per = (uint32_t)(p.prefix_len >> 6);
+    const uint32_t i = units / per;
+    return i * per == units ? (int64_t)i - 1 : -1;
+}
+
+}  // namespace gdn

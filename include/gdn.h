@@ -285,6 +285,237 @@ size_t gdn_prefill_workspace_size(int32_t num_seqs, int64_t tokens, int32_t Hk,
                                   int32_t Hv, int32_t Dk, int32_t Dv,
                                   gdn_dtype_t dtype, int32_t packed);
 
+/*
+ * Gated linear recurrence (the scan calls)
+ * ----------------------------------------
+ * The vector-state sibling of the gated delta rule: one state value per
+ * channel instead of a matrix per head. Per sequence and channel
+ *
+ *     h_t = alpha_t * h_{t-1} + beta_t * x_t,      out_t = h_t
+ *
+ * with a decay and a write strength of its own for every token and channel.
+ * x, alpha, beta and out have the element type `dtype`; states are fp32 [D]
+ * per sequence. beta == NULL ties the gates: beta_t = 1 - alpha_t. `flags`
+ * accepts GDN_GATE_LOGITS: alpha holds a, beta holds b, and the kernels use
+ * alpha = exp(-softplus(a)) = sigmoid(-a), beta = sigmoid(b) (tied:
+ * beta = sigmoid(a), formed without cancellation). Any other bit:
+ * GDN_ERR_UNSUPPORTED. Unlike the delta-rule calls, alpha is used as given
+ * (not clamped). 1 <= D <= 2^22; widths that are a multiple of 16 bytes run
+ * on 16-byte accesses.
+ */
+
+/* Tokens per tile of the scan kernels: block starts at multiples of this are
+ * where gdn_scan_backward picks up prefix states. */
+enum { GDN_SCAN_TILE = 128 };
+
+/*
+ * gdn_scan_prefill -- the recurrence over B equal-length sequences.
+ *
+ *   x, alpha, beta, out [B, T, D] dtype   (beta may be NULL: tied gates)
+ *   initial_state [B, D] fp32 or NULL (zero)
+ *   final_state   [B, D] fp32 or NULL; may equal initial_state
+ *   prefix_states [B * floor(T / L), D] fp32 or NULL: the state after every
+ *                 whole block of L = 64 * prefix_interval tokens, in the rows
+ *                 of gdn_prefill_chunked's prefix_states
+ *
+ * Sizes: B >= 1, T >= 0, D >= 1. T == 0 writes the initial state (or zeros) to
+ * final_state. workspace: optional device scratch (16-byte aligned, disjoint
+ * from every other argument, contents ignored and overwritten). With at least
+ * gdn_scan_workspace_size() bytes the call may cut the sequences along time
+ * and run the pieces side by side; NULL or less runs each sequence's tiles one
+ * after the other. Both give the same bits. Aliasing rules as for
+ * gdn_prefill_chunked.
+ */
+gdn_status_t gdn_scan_prefill(const void *x, const void *alpha, const void *beta,
+                              const float *initial_state, void *out, float *final_state,
+                              float *prefix_states, int32_t prefix_interval, int32_t B,
+                              int64_t T, int32_t D, gdn_dtype_t dtype, uint32_t flags,
+                              void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * gdn_scan_varlen_prefill -- the recurrence over N packed sequences.
+ *
+ *   x, alpha, beta, out [total_T, D] dtype
+ *   cu_seqlens          [N + 1] int32, DEVICE memory, as for
+ *                       gdn_varlen_prefill (clamped, checked under GDN_DEBUG=1)
+ *   initial_state, final_state [N, D] fp32 or NULL
+ *   prefix_states       [floor(total_T / L) + N, D] fp32 or NULL, in the rows
+ *                       of gdn_varlen_prefill's prefix_states
+ *
+ * A sequence of length zero hands its initial state (or zeros) to final_state.
+ * Each sequence's results have the same bits as gdn_scan_prefill's on it alone.
+ */
+gdn_status_t gdn_scan_varlen_prefill(const void *x, const void *alpha, const void *beta,
+                                     const int32_t *cu_seqlens, int32_t N, int64_t total_T,
+                                     const float *initial_state, void *out, float *final_state,
+                                     float *prefix_states, int32_t prefix_interval, int32_t D,
+                                     gdn_dtype_t dtype, uint32_t flags, void *workspace,
+                                     size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * gdn_scan_backward -- gradients of gdn_scan_prefill.
+ *
+ *   dout                [B, T, D] dtype: gradient of out
+ *   x, alpha, beta, initial_state: the forward call's inputs
+ *   prefix_states       [B * floor(T / L), D] fp32: as the forward call wrote
+ *                       them, with prefix_interval 1 or 2 (L = 64 or 128); the
+ *                       states inside a tile of GDN_SCAN_TILE tokens are
+ *                       recomputed from them in fp32. May be NULL when
+ *                       T <= GDN_SCAN_TILE.
+ *   dfinal              [B, D] fp32 or NULL (zero): gradient of final_state
+ *   dx, dalpha, dbeta   [B, T, D] dtype; dbeta is NULL exactly when beta is.
+ *                       With GDN_GATE_LOGITS dalpha and dbeta are the gradients
+ *                       of the logits. Tied gates: dalpha holds both paths.
+ *   dinitial            [B, D] fp32 or NULL: gradient of initial_state
+ *
+ * With g_t = dout_t + alpha_{t+1} g_{t+1} (from dfinal at the end):
+ *   dx_t = beta_t g_t, dbeta_t = g_t x_t, dalpha_t = g_t h_{t-1}
+ *   (tied: g_t (h_{t-1} - x_t)), dinitial = alpha_1 g_1.
+ * T == 0 copies dfinal (or zeros) to dinitial. Outputs overlap nothing.
+ * workspace: as for gdn_scan_prefill.
+ */
+gdn_status_t gdn_scan_backward(const void *dout, const void *x, const void *alpha,
+                               const void *beta, const float *initial_state,
+                               const float *prefix_states, int32_t prefix_interval,
+                               const float *dfinal, void *dx, void *dalpha, void *dbeta,
+                               float *dinitial, int32_t B, int64_t T, int32_t D,
+                               gdn_dtype_t dtype, uint32_t flags, void *workspace,
+                               size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * gdn_scan_varlen_backward -- gradients of gdn_scan_varlen_prefill: as above
+ * with [total_T, D] tensors, cu_seqlens, states [N, D] and the packed call's
+ * prefix rows (prefix_states may be NULL when total_T <= GDN_SCAN_TILE).
+ */
+gdn_status_t gdn_scan_varlen_backward(const void *dout, const void *x, const void *alpha,
+                                      const void *beta, const int32_t *cu_seqlens, int32_t N,
+                                      int64_t total_T, const float *initial_state,
+                                      const float *prefix_states, int32_t prefix_interval,
+                                      const float *dfinal, void *dx, void *dalpha, void *dbeta,
+                                      float *dinitial, int32_t D, gdn_dtype_t dtype,
+                                      uint32_t flags, void *workspace, size_t workspace_bytes,
+                                      hipStream_t stream);
+
+/*
+ * gdn_scan_decode -- K new tokens per sequence against a pool of state slots.
+ *
+ *   x, alpha, beta, out  [B, K, D] dtype (beta may be NULL)
+ *   state_pool           [num_slots, D] fp32
+ *   src_slot, dst_slot   [B] int32, DEVICE memory, with gdn_decode_multi's
+ *                        meaning and rules (negative: zero state / not
+ *                        written; past the pool: NaN outputs, no slot touched)
+ *
+ * Sizes: B >= 1, K >= 0, D >= 1. K == 0 copies slots.
+ */
+gdn_status_t gdn_scan_decode(const void *x, const void *alpha, const void *beta,
+                             float *state_pool, int32_t num_slots, const int32_t *src_slot,
+                             const int32_t *dst_slot, void *out, int32_t B, int32_t K,
+                             int32_t D, gdn_dtype_t dtype, uint32_t flags, hipStream_t stream);
+
+/*
+ * gdn_scan_workspace_size -- bytes of workspace the scan calls can use:
+ * packed = 0: num_seqs = B, tokens = T; packed = 1: num_seqs = N,
+ * tokens = total_T. 0 when the call would not use one (sequences of one tile,
+ * or enough of them to fill the device), when an argument is invalid, or when
+ * no device is available.
+ */
+size_t gdn_scan_workspace_size(int32_t num_seqs, int64_t tokens, int32_t D, gdn_dtype_t dtype,
+                               int32_t packed);
+
+/*
+ * gdn_rms_norm -- root-mean-square norm with the residual's addition and an
+ * output in 8 bits with scales: the step in front of the mixer's projections
+ * (with a residual) and behind the mixer per value head (rows of D = 128).
+ *
+ *   x        [rows, D] dtype
+ *   residual [rows, D] dtype or NULL (none)
+ *   weight   [D]       dtype
+ *   residual_out [rows, D] dtype or NULL (not written): r = x + residual,
+ *            rounded; may equal residual or x. Needs a residual.
+ *   out      [rows, D] dtype or NULL: y = r / sqrt(mean(r^2) + eps) * weight
+ *   out8     [rows, D] OCP e4m3 or NULL: y / scale, rounded to nearest even
+ *   scales   [rows, G] fp32, set exactly when out8 is. scale = max |y| / 448
+ *            over the group (at least 2^-100), so that out8 * scale stands
+ *            for y. group 0: one scale per row (G = 1); group 128: one per 128
+ *            columns (G = ceil(D / 128)); others: GDN_ERR_UNSUPPORTED.
+ *
+ * The sum, the mean and y are fp32; y is formed from the unrounded sum, and
+ * out8 from the unrounded y. Sizes: rows >= 0, 1 <= D <= 16384, eps > 0. At
+ * least one of out and out8. A NaN or Inf in a row makes NaN in that row.
+ */
+gdn_status_t gdn_rms_norm(const void *x, const void *residual, const void *weight,
+                          void *residual_out, void *out, void *out8, float *scales,
+                          int32_t group, int64_t rows, int32_t D, gdn_dtype_t dtype, float eps,
+                          hipStream_t stream);
+
+/*
+ * gdn_rms_norm_backward -- gradients of gdn_rms_norm's y at a stored row sum.
+ *
+ *   dout      [rows, D] dtype: gradient of y
+ *   r         [rows, D] dtype: the row sums (residual_out; x without a residual)
+ *   weight    [D] dtype
+ *   dresidual [rows, D] dtype or NULL: gradient arriving at residual_out
+ *   dx        [rows, D] dtype: gradient of x and of residual alike; may equal
+ *             dresidual
+ *   dweight   [D] fp32 or NULL (not wanted)
+ *
+ * With s = 1 / sqrt(mean(r^2) + eps):
+ *   dx = s w dout - r s^3 mean(w dout r) + dresidual,
+ *   dweight = sum over rows of dout r s (fp32, in a fixed order).
+ * workspace: gdn_rms_norm_workspace_size(rows, D) bytes, required with dweight
+ * (GDN_ERR_BAD_SHAPE when too small), unused without.
+ */
+gdn_status_t gdn_rms_norm_backward(const void *dout, const void *r, const void *weight,
+                                   const void *dresidual, void *dx, float *dweight,
+                                   int64_t rows, int32_t D, gdn_dtype_t dtype, float eps,
+                                   void *workspace, size_t workspace_bytes,
+                                   hipStream_t stream);
+size_t gdn_rms_norm_workspace_size(int64_t rows, int32_t D);
+
+/*
+ * gdn_beam_select -- beam search's selection over beams and vocabulary.
+ *
+ *   logits   [B, W, V] dtype: next-token logits of every beam
+ *   scores   [B, W] fp32: summed log-probability of every beam
+ *   finished [B, W] uint8 or NULL: nonzero beams have ended and offer only
+ *            themselves (token eos, score unchanged)
+ *   beam_slots [B, W] int32 or NULL: the state slot of every beam
+ *   new_scores [B, W] fp32, tokens [B, W] int32, parents [B, W] int32 (beam
+ *            index in its batch item): the W best candidates, best first
+ *   new_finished [B, W] uint8 or NULL: the parent's flag, or token == eos
+ *   src_slots [B, W] int32, set exactly when beam_slots is:
+ *            beam_slots[b][parent], the src_slot of the next
+ *            gdn_decode_multi or gdn_scan_decode call (states are reordered by
+ *            reading the parent's slot; give every beam a dst_slot that is no
+ *            beam's source), or the index of gdn_gather_states
+ *
+ * A live beam w offers every token v at score_w + logit - logsumexp(logits_w),
+ * compared in fp64; ties go to the lowest w * V + v. A beam whose score or
+ * logsumexp is not finite (all logits -inf, any NaN or +inf) offers its tokens
+ * at -inf, as does a logit of -inf. Sizes: B >= 1, 1 <= W <= 32, V >= 1,
+ * B * W * V < 2^40; eos in [0, V), or -1 for none (then finished and
+ * new_finished are NULL). Results are the same from call to call.
+ * workspace: gdn_beam_workspace_size() bytes, required.
+ */
+gdn_status_t gdn_beam_select(const void *logits, const float *scores, const uint8_t *finished,
+                             const int32_t *beam_slots, float *new_scores, int32_t *tokens,
+                             int32_t *parents, uint8_t *new_finished, int32_t *src_slots,
+                             int32_t B, int32_t W, int64_t V, int32_t eos, gdn_dtype_t dtype,
+                             void *workspace, size_t workspace_bytes, hipStream_t stream);
+size_t gdn_beam_workspace_size(int32_t B, int32_t W, int64_t V, gdn_dtype_t dtype);
+
+/*
+ * gdn_gather_states -- rows of a state buffer in a new order: row i of dst is
+ * row index[i] of src. For callers whose states are not addressed by slots.
+ *
+ *   src [num_src, row_bytes], dst [rows, row_bytes], index [rows] int32 in
+ *   DEVICE memory. row_bytes: a multiple of 16. A negative index writes zeros,
+ *   one past the end writes bytes of 0xff (NaN as fp32 or bf16). src and dst
+ *   must not overlap (an in-place permutation would need a copy).
+ */
+gdn_status_t gdn_gather_states(const void *src, int64_t num_src, const int32_t *index, void *dst,
+                               int64_t rows, int64_t row_bytes, hipStream_t stream);
+
 /* Static description of a status; for GDN_ERR_HIP, the calling thread's
  * last HIP error detail. The pointer stays valid until the thread's next
  * call into the library. */

@@ -1,0 +1,200 @@
+"""The RMS norm with residual and 8-bit output, and its gradients, against
+64-bit forms.
+
+Roundings counted for the tolerances: the sum of squares is a tree over
+per-thread chains of at most 16 terms plus 10 levels, each addition half a unit
+of 2^-24 relative to a sum of positive terms, halved by the square root, then
+the division, the square root's own and two products: y stays within
+32 * 2^-24 = 2^-19 relative, and so do the scales (one more division).
+"""
+import pytest
+
+torch = pytest.importorskip("torch")
+from tests.ops_oracle import U32, half_step, norm64, norm_backward64  # noqa: E402
+
+DEV = "cuda:0"
+gpu = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+REL = 32 * U32
+
+
+@pytest.fixture(scope="module")
+def gdn():
+    import gated_deltanet_token_amd as g
+    g.load_library()
+    return g
+
+
+def inputs(seed, rows, D, dtype, res=True):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(rows, D, generator=g).to(dtype)
+    w = (1 + 0.3 * torch.randn(D, generator=g)).to(dtype)
+    r = (torch.randn(rows, D, generator=g) * 3).to(dtype) if res else None
+    return x, w, r
+
+
+def dev(*ts):
+    return [None if t is None else t.to(DEV) for t in ts]
+
+
+def check_y(got, y, dtype):
+    tol = REL * y.abs() + (half_step(dtype) * y.abs() * (1 + REL) if dtype != torch.float32 else 0)
+    assert ((got.cpu().double() - y).abs() <= tol + 1e-37).all()
+
+
+def check_8bit(q, scale, y, group):
+    """q * scale stands for y: scales to REL, values to half a step of e4m3 (2^-4 relative,
+    2^-10 below the smallest normal)."""
+    D = y.shape[-1]
+    cols = group or D
+    scale = scale.cpu().double()
+    for i, part in enumerate(y.split(cols, -1)):
+        want = (part.abs().amax(-1) / 448).clamp(min=2.0 ** -100)
+        assert ((scale[..., i] - want).abs() <= REL * want).all()
+        got = q[..., i * cols:i * cols + part.shape[-1]].cpu().float().double()
+        s = scale[..., i:i + 1]
+        tol = part.abs() * (2.0 ** -4 * (1 + 2.0 ** -10) + 4 * REL) + s * 2.0 ** -10
+        assert ((got * s - part).abs() <= tol).all()
+        # the largest value of a group is the largest e4m3 value (or the group is zero)
+        top = got.abs().amax(-1)
+        assert ((top == 448) | (part.abs().amax(-1) < 448 * 2.0 ** -100)).all()
+
+
+SHAPES = [(1, 1), (3, 7), (5, 8), (17, 64), (33, 100), (16, 128), (70, 129), (9, 200), (4, 512),
+          (3, 520), (2, 1027), (7, 2048), (3, 5120), (2, 8192), (2, 8200), (1, 9001), (2, 16384),
+          (1000, 128), (1, 16383)]
+
+
+@gpu
+@pytest.mark.parametrize("rows,D", SHAPES, ids=str)
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("res", [False, True])
+def test_norm(gdn, rows, D, dt, res):
+    dtype = DT[dt]
+    x, w, r = inputs(rows * 31 + D, rows, D, dtype, res)
+    xd, wd, rd = dev(x, w, r)
+    total, s, y = norm64(x, w, r, 1e-6)
+    for group in (0, 128):
+        out, q, scale, ro = gdn.gdn_rms_norm(xd, wd, rd, group=group, want_out8=True)
+        check_y(out, y, dtype)
+        check_8bit(q, scale, y, group)
+        assert (ro is None) == (not res)
+        if res:  # the sum is rounded to fp32, then to the type
+            tol = total.abs() * (half_step(dtype) * (1 + U32) + U32)
+            assert ((ro.cpu().double() - total).abs() <= tol).all()
+    # each output alone gives the same bits
+    o1, none, none2, _ = gdn.gdn_rms_norm(xd, wd, rd)
+    assert none is None and none2 is None and torch.equal(o1, out)
+    none, q1, s1, ro1 = gdn.gdn_rms_norm(xd, wd, rd, group=128, want_out=False, want_out8=True,
+                                         want_residual=False)
+    assert none is None and ro1 is None
+    assert torch.equal(q1.view(torch.uint8), q.view(torch.uint8)) and torch.equal(s1, scale)
+
+
+@gpu
+def test_residual_in_place_and_leading_dims(gdn):
+    x, w, r = inputs(1, 30, 256, torch.bfloat16)
+    xd, wd, rd = dev(x, w, r)
+    want = gdn.gdn_rms_norm(xd, wd, rd)
+    mine = rd.clone()
+    out, _, _, ro = gdn.gdn_rms_norm(xd.view(2, 3, 5, 256), wd, mine.view(2, 3, 5, 256),
+                                     residual_out=mine.view(2, 3, 5, 256))
+    assert torch.equal(out.view(30, 256), want[0]) and torch.equal(mine, want[3])
+    mine = xd.clone()
+    gdn.gdn_rms_norm(mine, wd, rd, residual_out=mine)
+    assert torch.equal(mine, want[3])
+
+
+@gpu
+def test_zero_rows_and_zero_values(gdn):
+    w = torch.ones(128, device=DEV)
+    out, q, s, _ = gdn.gdn_rms_norm(torch.empty(0, 128, device=DEV), w, want_out8=True)
+    assert out.shape == (0, 128) and q.shape == (0, 128) and s.shape == (0, 1)
+    x = torch.zeros(2, 128, device=DEV)
+    x[1, 3] = 5.0
+    for group in (0, 128):
+        out, q, s, _ = gdn.gdn_rms_norm(x, w, want_out8=True, group=group)
+        assert (out[0] == 0).all() and (q.float()[0] == 0).all() and s[0, 0] == 2.0 ** -100
+        assert q.float()[1, 3] == 448 and (q.float()[1] != 0).sum() == 1
+    dx, dw = gdn.gdn_rms_norm_backward(torch.empty(0, 128, device=DEV),
+                                       torch.empty(0, 128, device=DEV), w)
+    assert dx.shape == (0, 128) and (dw == 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("D", [128, 300, 2048, 1001])
+def test_nan_and_inf_stay_in_their_row(gdn, D):
+    x, w, r = inputs(4, 9, D, torch.float32)
+    xd, wd, rd = dev(x, w, r)
+    clean = gdn.gdn_rms_norm(xd, wd, rd, want_out8=True)
+    xd[2, D // 2] = float("nan")
+    xd[5, 1] = float("inf")
+    out, q, s, _ = gdn.gdn_rms_norm(xd, wd, rd, want_out8=True)
+    assert out[2].isnan().all() and q.float()[2].isnan().all()
+    assert out[5].isnan().any() and q.float()[5].isnan().any()
+    keep = [i for i in range(9) if i not in (2, 5)]
+    assert torch.equal(out[keep], clean[0][keep]) and torch.equal(s[keep], clean[2][keep])
+    assert torch.equal(q[keep].view(torch.uint8), clean[1][keep].view(torch.uint8))
+
+
+@gpu
+@pytest.mark.parametrize("rows,D", SHAPES + [(600, 264), (1300, 4096), (5000, 40)], ids=str)
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("res", [False, True])
+def test_backward(gdn, rows, D, dt, res):
+    dtype = DT[dt]
+    r, w, dres = inputs(rows * 13 + D, rows, D, dtype, res)
+    dy = torch.randn(rows, D, generator=torch.Generator().manual_seed(7)).to(dtype)
+    rd, wd, dyd, drd = dev(r, w, dy, dres)
+    dx, dw = gdn.gdn_rms_norm_backward(dyd, rd, wd, drd, eps=1e-5)
+    dx2, dw2 = gdn.gdn_rms_norm_backward(dyd, rd, wd, drd, eps=1e-5)
+    assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+    want, want_w, mag, mag_w = norm_backward64(dy, r, w, dres, 1e-5)
+    tol = 2 * REL * mag + (half_step(dtype) * want.abs() * (1 + REL) if dt == "bf16" else 0)
+    assert ((dx.cpu().double() - want).abs() <= tol + 1e-37).all()
+    # rows are summed in chains of at most rows / 16 per thread and 40 joins behind them
+    tol = (REL + U32 * (min(rows, rows / 16 + 80) + 40)) * mag_w
+    assert ((dw.cpu().double() - want_w).abs() <= tol + 1e-37).all()
+    # without the weight's gradient, and into dresidual itself
+    dx3, none = gdn.gdn_rms_norm_backward(dyd, rd, wd, drd, eps=1e-5, want_dweight=False)
+    assert none is None and torch.equal(dx3, dx)
+    if res:
+        mine = drd.clone()
+        gdn.gdn_rms_norm_backward(dyd, rd, wd, mine, eps=1e-5, dx=mine)
+        assert torch.equal(mine, dx)
+
+
+def test_the_formula_is_the_derivative():
+    g = torch.Generator().manual_seed(2)
+    r, w, dy, dres = [torch.randn(*s, generator=g).double() for s in ((3, 6), (6,), (3, 6), (3, 6))]
+    dx, dw, _, _ = norm_backward64(dy, r, w, dres, 1e-3)
+    loss = lambda: float((norm64(r, w, None, 1e-3)[2] * dy).sum() + (r * dres).sum())  # noqa: E731
+    for t, grad in ((r, dx), (w, dw)):
+        for i in range(t.numel()):
+            keep = t.view(-1)[i].item()
+            t.view(-1)[i] = keep + 1e-5
+            up = loss()
+            t.view(-1)[i] = keep - 1e-5
+            down = loss()
+            t.view(-1)[i] = keep
+            assert abs((up - down) / 2e-5 - float(grad.view(-1)[i])) < 1e-6
+
+
+@gpu
+def test_backward_against_differences(gdn):
+    """The kernels' own loss along a direction, fp32, against their gradients."""
+    step = 2.0 ** -7
+    r, w, _ = inputs(11, 20, 200, torch.float32, False)
+    g = torch.Generator().manual_seed(12)
+    dy = torch.randn(20, 200, generator=g)
+    dr, dw = torch.randn(20, 200, generator=g), torch.randn(200, generator=g)
+    gx, gw = gdn.gdn_rms_norm_backward(*dev(dy, r, w))
+    lin = (gx.cpu().double() * dr.double()).sum() + (gw.cpu().double() * dw.double()).sum()
+    y = lambda s: gdn.gdn_rms_norm(*dev(r + s * step * dr, w + s * step * dw))[0]  # noqa: E731
+    diff = ((y(1) - y(-1)).cpu().double() * dy.double()).sum() / (2 * step)
+    exact = lambda s: norm64(r.double() + s * step * dr.double(),  # noqa: E731
+                             w.double() + s * step * dw.double(), None, 1e-6)[2]
+    curve = abs(((exact(1) - exact(-1)) * dy.double()).sum() / (2 * step) - lin)
+    noise = 4 * REL * (exact(1).abs() * dy.double().abs()).sum() / (2 * step)
+    assert abs(diff - lin) <= curve + noise
+    assert curve <= 0.05 * abs(lin) + 1.0
