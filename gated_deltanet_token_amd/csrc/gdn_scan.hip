@@ -18,15 +18,53 @@ namespace gdn {
 
 namespace {
 
-// One workgroup per (sequence, column block), its tiles in order.
-template <typename DT, int VEC, bool TIED, bool LOGITS>
+// The tile that a workgroup of a SPLIT launch takes: its sequence, column block
+// and tile (whose count is `tiles`; a tile at or past it does not exist).
+struct ScanTile {
+    int n, cb;
+    int64_t slot, tile;
+};
+template <bool BACK>
+__device__ __forceinline__ ScanTile take_tile(const ScanParams &p, const ScanSplit &sp, int ncb,
+                                              int *s_ticket) {
+    const int chain = blockIdx.x % sp.chains;
+    if (threadIdx.x == 0)
+        *s_ticket = (int)__hip_atomic_fetch_add(sp.ticket + chain, 1u, __ATOMIC_RELAXED,
+                                                __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    int64_t k = *s_ticket;
+    ScanTile t;
+    if (p.cu) {
+        if (BACK) k = sp.slots - 1 - k;
+        t.cb = chain;
+        t.slot = k;
+        t.n = scan_slot_sequence(p, k);
+        int64_t base = p.cu[t.n];
+        base = base < 0 ? 0 : (base > p.total ? p.total : base);
+        t.tile = k - (base / GDN_SCAN_TILE + t.n);
+    } else {
+        if (BACK) k = sp.slots / p.N - 1 - k;
+        t.n = chain / ncb;
+        t.cb = chain - t.n * ncb;
+        t.tile = k;
+        t.slot = k * p.N + t.n;
+    }
+    return t;
+}
+
+// SPLIT: one tile per workgroup. Else one workgroup per (sequence, column
+// block), its tiles in order.
+template <typename DT, int VEC, bool TIED, bool LOGITS, bool SPLIT>
 __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_forward_kernel(
-    ScanParams p, int ncb) {
+    ScanParams p, int ncb, ScanSplit sp) {
     using Sh = ScanShape<DT, VEC>;
     constexpr int G = Sh::kGroups, C = Sh::kCols, R = Sh::kPer;
     __shared__ float s_a[G][C], s_h[G][C];
 
-    const int n = blockIdx.x / ncb, cb = blockIdx.x - n * ncb;
+    __shared__ int s_ticket;
+    ScanTile mine{(int)(blockIdx.x / ncb), (int)(blockIdx.x % ncb), 0, 0};
+    if constexpr (SPLIT) mine = take_tile<false>(p, sp, ncb, &s_ticket);
+    const int n = mine.n, cb = mine.cb;
     const int tid = threadIdx.x, g = tid / Sh::kLanes, l = tid % Sh::kLanes;
     const int D = p.D, c0 = cb * C + l * VEC;
     const bool on = c0 < D;
@@ -35,15 +73,17 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_forward_k
     const bool chain = tid < C && ch < D;
     int64_t base, len;
     scan_bounds(p, n, base, len);
-    float carry = 0.f;
-    if (chain && p.h0) carry = p.h0[(int64_t)n * D + ch];
-    if (len == 0) {
-        if (chain && p.hT) p.hT[(int64_t)n * D + ch] = carry;
+    float carry = 0.f;  // the state in front of the tile, once it is known
+    if (chain && p.h0 && mine.tile == 0) carry = p.h0[(int64_t)n * D + ch];
+    if (mine.tile < 0 || mine.tile * Sh::kRows >= len) {  // (below 0: malformed offsets)
+        if (mine.tile == 0 && chain && p.hT) p.hT[(int64_t)n * D + ch] = carry;
+        if constexpr (SPLIT)
+            if (tid < C) publish(sp.inc + mine.slot * sp.width + ch, 0u);
         return;
     }
     const int64_t prow = p.prefix_out ? scan_prefix_row(p, n, base) : 0;
 
-    for (int64_t t0 = 0; t0 < len; t0 += Sh::kRows) {
+    for (int64_t t0 = mine.tile * Sh::kRows; t0 < len; t0 += Sh::kRows) {
         const int left = (int)(len - t0 < Sh::kRows ? len - t0 : Sh::kRows);  // tokens here
         const int64_t tile = (base + t0) * D;
         const DT *xt = as<DT>(p.x, tile), *at = as<DT>(p.a, tile);
@@ -63,7 +103,7 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_forward_k
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 float alpha, keep, beta;
-                gates<TIED, LOGITS>(a[r][e], b[r][e], alpha, keep, beta);
+                gates<DT, TIED, LOGITS>(a[r][e], b[r][e], alpha, keep, beta);
                 al[r][e] = in ? alpha : 1.f;  // past the end: the identity
                 u[r][e] = in ? beta * x[r][e] : 0.f;
             }
@@ -81,14 +121,27 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_forward_k
         }
         __syncthreads();
         if (tid < C) {
-            float A = 1.f, H = 0.f, h = carry;
-#pragma unroll 4
+            float A = 1.f, H = 0.f;
+#pragma unroll 8
             for (int i = 0; i < G; ++i) {
-                const float ga = s_a[i][tid], gh = s_h[i][tid];
+                H = fmaf(s_a[i][tid], H, s_h[i][tid]);
+                A *= s_a[i][tid];
+            }
+            if constexpr (SPLIT) {
+                const int64_t at = mine.slot * sp.width + ch;
+                if (mine.tile > 0) {
+                    publish(sp.agg + at, scan_pair(A, H));
+                    const int64_t step = p.cu ? -1 : -(int64_t)p.N;
+                    carry = scan_look(sp, mine.slot + step, step, (int32_t)mine.tile, ch);
+                }
+                publish(sp.inc + at, scan_word(fmaf(A, carry, H)));
+            }
+            float h = carry;
+#pragma unroll 8
+            for (int i = 0; i < G; ++i) {
+                const float gh = s_h[i][tid];
                 s_h[i][tid] = h;  // the state in front of group i
-                h = fmaf(ga, h, gh);
-                H = fmaf(ga, H, gh);
-                A *= ga;
+                h = fmaf(s_a[i][tid], h, gh);
             }
             carry = fmaf(A, carry, H);
         }
@@ -116,17 +169,21 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_forward_k
         }
         if (on && p.hT && t0 + left == len && g == (left - 1) / R)
             store_raw(p.hT + (int64_t)n * D, c0 * 4, h);
+        if constexpr (SPLIT) return;
     }
 }
 
-template <typename DT, int VEC, bool TIED, bool LOGITS>
+template <typename DT, int VEC, bool TIED, bool LOGITS, bool SPLIT>
 __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_backward_kernel(
-    ScanParams p, int ncb) {
+    ScanParams p, int ncb, ScanSplit sp) {
     using Sh = ScanShape<DT, VEC>;
     constexpr int G = Sh::kGroups, C = Sh::kCols, R = Sh::kPer;
     __shared__ float s_a[G][C], s_h[G][C], s_k[G][C];
 
-    const int n = blockIdx.x / ncb, cb = blockIdx.x - n * ncb;
+    __shared__ int s_ticket;
+    ScanTile mine{(int)(blockIdx.x / ncb), (int)(blockIdx.x % ncb), 0, 0};
+    if constexpr (SPLIT) mine = take_tile<true>(p, sp, ncb, &s_ticket);
+    const int n = mine.n, cb = mine.cb;
     const int tid = threadIdx.x, g = tid / Sh::kLanes, l = tid % Sh::kLanes;
     const int D = p.D, c0 = cb * C + l * VEC;
     const bool on = c0 < D;
@@ -135,11 +192,19 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_backward_
     const bool chain = tid < C && ch < D;
     int64_t base, len;
     scan_bounds(p, n, base, len);
-    float carry = 0.f;
-    if (chain && p.dhT) carry = p.dhT[(int64_t)n * D + ch];
+    const int64_t last = len > 0 ? (len - 1) / Sh::kRows : 0;
+    if constexpr (!SPLIT) mine.tile = last;
+    float carry = 0.f;  // what reaches the tile from behind, once it is known
+    if (chain && p.dhT && mine.tile == last) carry = p.dhT[(int64_t)n * D + ch];
+    if (mine.tile < 0 || mine.tile * Sh::kRows >= len) {  // (below 0: malformed offsets)
+        if (mine.tile == 0 && chain && p.dh0) p.dh0[(int64_t)n * D + ch] = carry;
+        if constexpr (SPLIT)
+            if (tid < C) publish(sp.inc + mine.slot * sp.width + ch, 0u);
+        return;
+    }
     const int64_t prow = p.prefix_in ? scan_prefix_row(p, n, base) : 0;
 
-    for (int64_t t0 = (len - 1) / Sh::kRows * Sh::kRows; len > 0 && t0 >= 0; t0 -= Sh::kRows) {
+    for (int64_t t0 = mine.tile * Sh::kRows; t0 >= 0; t0 -= Sh::kRows) {
         const int left = (int)(len - t0 < Sh::kRows ? len - t0 : Sh::kRows);
         const int64_t tile = (base + t0) * D;
         const DT *xt = as<DT>(p.x, tile), *at = as<DT>(p.a, tile), *yt = as<DT>(p.dout, tile);
@@ -167,7 +232,7 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_backward_
             for (int r = 0; r < R; ++r) {
                 const bool in = g * R + r < left;
                 float alpha, keep, beta;
-                gates<TIED, LOGITS>(a[r][e], b[r][e], alpha, keep, beta);
+                gates<DT, TIED, LOGITS>(a[r][e], b[r][e], alpha, keep, beta);
                 alpha = in ? alpha : 1.f;
                 H = fmaf(alpha, H, in ? beta * x[r][e] : 0.f);
                 // rows join at the far end: K = sum of dy_r times the decays up to it
@@ -180,21 +245,35 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_backward_
         }
         __syncthreads();
         if (tid < C) {
+            float A = 1.f, K = 0.f;
+#pragma unroll 8
+            for (int i = G - 1; i >= 0; --i) {
+                K = fmaf(s_a[i][tid], K, s_k[i][tid]);
+                A *= s_a[i][tid];
+            }
+            if constexpr (SPLIT) {
+                if (mine.tile < last) publish(sp.agg + mine.slot * sp.width + ch, scan_pair(A, K));
+            }
             float h = h_in;
-#pragma unroll 4
+#pragma unroll 8
             for (int i = 0; i < G; ++i) {
                 const float gh = s_h[i][tid];
                 s_h[i][tid] = h;
                 h = fmaf(s_a[i][tid], h, gh);
             }
-            float A = 1.f, K = 0.f, c = carry;
-#pragma unroll 4
+            if constexpr (SPLIT) {
+                if (mine.tile < last) {
+                    const int64_t step = p.cu ? 1 : p.N;
+                    carry = scan_look(sp, mine.slot + step, step, (int32_t)(last - mine.tile), ch);
+                }
+                publish(sp.inc + mine.slot * sp.width + ch, scan_word(fmaf(A, carry, K)));
+            }
+            float c = carry;
+#pragma unroll 8
             for (int i = G - 1; i >= 0; --i) {
-                const float ga = s_a[i][tid], gk = s_k[i][tid];
+                const float gk = s_k[i][tid];
                 s_k[i][tid] = c;  // what reaches group i from behind
-                c = fmaf(ga, c, gk);
-                K = fmaf(ga, K, gk);
-                A *= ga;
+                c = fmaf(s_a[i][tid], c, gk);
             }
             carry = fmaf(A, carry, K);
         }
@@ -209,7 +288,7 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_backward_
             for (int r = 0; r < R; ++r) {
                 float alpha, keep, beta;
                 before[r].v[e] = h;
-                gates<TIED, LOGITS>(a[r][e], b[r][e], alpha, keep, beta);
+                gates<DT, TIED, LOGITS>(a[r][e], b[r][e], alpha, keep, beta);
                 h = fmaf(alpha, h, beta * x[r][e]);
             }
         }
@@ -224,8 +303,8 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_backward_
             for (int r = R - 1; r >= 0; --r) {
                 const bool in = g * R + r < left;  // past the end c passes through
                 float alpha, keep, beta, rest = 0.f;
-                gates<TIED, LOGITS>(a[r][e], b[r][e], alpha, keep, beta);
-                if constexpr (!TIED && LOGITS) sigmoid_pair(-b[r][e], beta, rest);
+                gates<DT, TIED, LOGITS>(a[r][e], b[r][e], alpha, keep, beta);
+                if constexpr (!TIED && LOGITS) sigmoid_pair<DT>(-b[r][e], beta, rest);
                 const float gr = (in ? dy[r][e] : 0.f) + c;
                 c = (in ? alpha : 1.f) * gr;
                 // alpha' = -alpha (1 - alpha), beta' = beta (1 - beta) of the logits
@@ -249,6 +328,9 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_backward_
             store_raw(dxt, i, x[r]);
             store_raw(dat, i, a[r]);
             if constexpr (!TIED) store_raw(dbt, i, b[r]);
+        }
+        if constexpr (SPLIT) {
+            if (mine.tile > 0) return;
         }
     }
     if (chain && p.dh0) p.dh0[(int64_t)n * D + ch] = carry;
@@ -278,7 +360,7 @@ __global__ __launch_bounds__(256) void scan_decode_kernel(ScanDecodeParams p) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             float alpha, keep, beta;
-            gates<TIED, LOGITS>(a[e], w[e], alpha, keep, beta);
+            gates<DT, TIED, LOGITS>(a[e], w[e], alpha, keep, beta);
             h.v[e] = fmaf(alpha, h[e], beta * x[e]);
             o.set(e, h[e]);
         }
@@ -309,24 +391,102 @@ template <typename DT, int VEC> int column_blocks(int32_t D) {
     return (D + ScanShape<DT, VEC>::kCols - 1) / ScanShape<DT, VEC>::kCols;
 }
 
+// Sets a SPLIT launch's workspace: counters to 0, words to absent.
+__global__ __launch_bounds__(256) void scan_clear_kernel(u32x4 *ws, int64_t zero, int64_t total) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
+         i += (int64_t)gridDim.x * 256) {
+        const uint32_t v = i < zero ? 0u : kAbsent;
+        ws[i] = u32x4{v, v, v, v};
+    }
+}
+
+// The workspace of a SPLIT launch: counters, then inc, then agg.
+struct ScanLayout {
+    int64_t chains, slots, width, words_at, bytes;
+};
+
+ScanLayout scan_layout(int64_t nseq, int64_t tokens, int32_t D, int cols, bool packed) {
+    ScanLayout l;
+    const int64_t ncb = (D + cols - 1) / cols;
+    l.width = ncb * cols;
+    l.chains = packed ? ncb : nseq * ncb;
+    l.slots = packed ? tokens / GDN_SCAN_TILE + nseq
+                     : nseq * ((tokens + GDN_SCAN_TILE - 1) / GDN_SCAN_TILE);
+    l.words_at = (l.chains * 4 + 255) / 256 * 256;
+    l.bytes = l.words_at + l.slots * l.width * 12;
+    return l;
+}
+
+// Whether a call is cut along time: sequences of more than one tile, and not
+// enough (sequence, column block) pairs to fill the device with one workgroup
+// each.
+bool scan_wants_split(int64_t nseq, int64_t tokens, int64_t ncb, bool packed, int cus) {
+    (void)packed;
+    return tokens > GDN_SCAN_TILE && nseq * ncb < 8 * (int64_t)cus;
+}
+
+int scan_cols(int32_t D, int dtype) {
+    if (dtype == 1) return D % 8 == 0 ? ScanShape<__bf16, 8>::kCols : ScanShape<__bf16, 1>::kCols;
+    return D % 4 == 0 ? ScanShape<float, 4>::kCols : ScanShape<float, 1>::kCols;
+}
+
+// Fills sp and clears the workspace when the call is to be cut; sp.slots is 0
+// when not.
+hipError_t prepare_split(const ScanParams &p, int dtype, int cus, void *ws, size_t ws_bytes,
+                         ScanSplit &sp, hipStream_t stream) {
+    sp = ScanSplit{};
+    const bool packed = p.cu != nullptr;
+    const int64_t tokens = packed ? p.total : p.T;
+    const int cols = scan_cols(p.D, dtype);
+    const ScanLayout l = scan_layout(p.N, tokens, p.D, cols, packed);
+    if (!ws || ws_bytes < (size_t)l.bytes ||
+        !scan_wants_split(p.N, tokens, l.width / cols, packed, cus))
+        return hipSuccess;
+    char *base = static_cast<char *>(ws);
+    sp.ticket = reinterpret_cast<uint32_t *>(base);
+    sp.agg = reinterpret_cast<uint64_t *>(base + l.words_at);
+    sp.inc = reinterpret_cast<uint32_t *>(sp.agg + l.slots * l.width);
+    sp.chains = (int32_t)l.chains;
+    sp.slots = (int32_t)l.slots;
+    sp.width = (int32_t)l.width;
+    const int64_t total = (l.bytes + 15) / 16, wgs = (total + 1023) / 1024;
+    hipLaunchKernelGGL(scan_clear_kernel, dim3((unsigned)(wgs < 2048 ? wgs : 2048)), dim3(256), 0,
+                       stream, static_cast<u32x4 *>(ws), l.words_at / 16, total);
+    return hipGetLastError();
+}
+
 struct RunForward {
     const ScanParams &p;
+    const ScanSplit &sp;
     hipStream_t stream;
     template <typename DT, int VEC, bool TIED, bool LOGITS> hipError_t run() const {
         const int ncb = column_blocks<DT, VEC>(p.D);
-        hipLaunchKernelGGL((scan_forward_kernel<DT, VEC, TIED, LOGITS>), dim3((unsigned)(p.N * ncb)),
-                           dim3(ScanShape<DT, VEC>::kThreads), 0, stream, p, ncb);
+        const dim3 block(ScanShape<DT, VEC>::kThreads);
+        if (sp.slots > 0)
+            hipLaunchKernelGGL((scan_forward_kernel<DT, VEC, TIED, LOGITS, true>),
+                               dim3((unsigned)((int64_t)sp.slots * ncb)), block, 0, stream, p,
+                               ncb, sp);
+        else
+            hipLaunchKernelGGL((scan_forward_kernel<DT, VEC, TIED, LOGITS, false>),
+                               dim3((unsigned)(p.N * ncb)), block, 0, stream, p, ncb, sp);
         return hipGetLastError();
     }
 };
 
 struct RunBackward {
     const ScanParams &p;
+    const ScanSplit &sp;
     hipStream_t stream;
     template <typename DT, int VEC, bool TIED, bool LOGITS> hipError_t run() const {
         const int ncb = column_blocks<DT, VEC>(p.D);
-        hipLaunchKernelGGL((scan_backward_kernel<DT, VEC, TIED, LOGITS>), dim3((unsigned)(p.N * ncb)),
-                           dim3(ScanShape<DT, VEC>::kThreads), 0, stream, p, ncb);
+        const dim3 block(ScanShape<DT, VEC>::kThreads);
+        if (sp.slots > 0)
+            hipLaunchKernelGGL((scan_backward_kernel<DT, VEC, TIED, LOGITS, true>),
+                               dim3((unsigned)((int64_t)sp.slots * ncb)), block, 0, stream, p,
+                               ncb, sp);
+        else
+            hipLaunchKernelGGL((scan_backward_kernel<DT, VEC, TIED, LOGITS, false>),
+                               dim3((unsigned)(p.N * ncb)), block, 0, stream, p, ncb, sp);
         return hipGetLastError();
     }
 };
@@ -344,15 +504,28 @@ struct RunDecode {
 
 }  // namespace
 
-size_t scan_workspace_bytes(int64_t, int64_t, int32_t, int, bool, int) { return 0; }
-
-hipError_t launch_scan(const ScanParams &p, int dtype, int, void *, size_t, hipStream_t stream) {
-    return with_scan_types(dtype, p.D, p.b, p.flags, RunForward{p, stream});
+size_t scan_workspace_bytes(int64_t nseq, int64_t tokens, int32_t D, int dtype, bool packed,
+                            int cus) {
+    const int cols = scan_cols(D, dtype);
+    const ScanLayout l = scan_layout(nseq, tokens, D, cols, packed);
+    if (!scan_wants_split(nseq, tokens, l.width / cols, packed, cus)) return 0;
+    return (size_t)((l.bytes + 15) / 16 * 16);
 }
 
-hipError_t launch_scan_backward(const ScanParams &p, int dtype, int, void *, size_t,
-                                hipStream_t stream) {
-    return with_scan_types(dtype, p.D, p.b, p.flags, RunBackward{p, stream});
+hipError_t launch_scan(const ScanParams &p, int dtype, int cus, void *ws, size_t ws_bytes,
+                       hipStream_t stream) {
+    ScanSplit sp;
+    const hipError_t e = prepare_split(p, dtype, cus, ws, ws_bytes, sp, stream);
+    if (e != hipSuccess) return e;
+    return with_scan_types(dtype, p.D, p.b, p.flags, RunForward{p, sp, stream});
+}
+
+hipError_t launch_scan_backward(const ScanParams &p, int dtype, int cus, void *ws,
+                                size_t ws_bytes, hipStream_t stream) {
+    ScanSplit sp;
+    const hipError_t e = prepare_split(p, dtype, cus, ws, ws_bytes, sp, stream);
+    if (e != hipSuccess) return e;
+    return with_scan_types(dtype, p.D, p.b, p.flags, RunBackward{p, sp, stream});
 }
 
 hipError_t launch_scan_decode(const ScanDecodeParams &p, int dtype, hipStream_t stream) {

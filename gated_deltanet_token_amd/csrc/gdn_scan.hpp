@@ -52,10 +52,11 @@ __device__ __forceinline__ void forget_all(Raw<DT, VEC> (&x)[R]) {
     for (int r = 0; r < R; ++r) forget(x[r]);
 }
 
-// e^z for z in [-110, 80] (held there outside), the product z log2(e) carried in two terms (Cody and
-// Waite's reduction in base 2): a plain product would be off by |z| 2^-24, and
-// the small gates 1 - alpha inherit that error whole.
-__device__ __forceinline__ float exp_two_term(float z) {
+// Gates of fp32 logits: e^z for z in [-110, 80] (held there outside), the
+// product z log2(e) carried in two terms (Cody and Waite's reduction in base
+// 2): a plain product would be off by |z| 2^-24, and the small gates 1 - alpha
+// inherit that error whole.
+__device__ __forceinline__ float exp_logit(float z, float) {
     constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0bep-26f, kLn2 = 0x1.62e430p-1f;
     z = z > 80.f ? 80.f : z;  // keeps 1 + e^z finite; a NaN stays one
     z = z < -110.f ? -110.f : z;  // e^z is 0 there, and the product stays finite
@@ -64,13 +65,18 @@ __device__ __forceinline__ float exp_two_term(float z) {
     const float e = __builtin_amdgcn_exp2f(t);
     return fmaf(e, low * kLn2, e);
 }
+// Of bf16 logits: the plain product. Its error, |z| 2^-24 at the most, is far
+// below that of the outputs' rounding to bf16 (2^-9), and the forward kernel is
+// short of vector instructions.
+__device__ __forceinline__ float exp_logit(float z, __bf16) {
+    return __builtin_amdgcn_exp2f((z > 80.f ? 80.f : z) * 0x1.715476p+0f);
+}
 
-// s = 1 / (1 + e^z) and its complement e^z / (1 + e^z), each to about one
-// unit in its own last place: the reciprocal takes one Newton step, because
-// the errors of an alpha near 1 add up over its memory of 1 / (1 - alpha)
-// tokens.
-__device__ __forceinline__ void sigmoid_pair(float z, float &s, float &c) {
-    const float e = exp_two_term(z);
+// s = 1 / (1 + e^z) and its complement e^z / (1 + e^z): the reciprocal takes
+// one Newton step, because the errors of an alpha near 1 add up over its
+// memory of 1 / (1 - alpha) tokens.
+template <typename DT> __device__ __forceinline__ void sigmoid_pair(float z, float &s, float &c) {
+    const float e = exp_logit(z, DT());
     const float d = 1.f + e;
     float r = __builtin_amdgcn_rcpf(d);
     r = fmaf(r, fmaf(-d, r, 1.f), r);
@@ -78,16 +84,24 @@ __device__ __forceinline__ void sigmoid_pair(float z, float &s, float &c) {
     c = e * r;
 }
 
+// beta = 1 / (1 + e^-b), whose errors do not add up: of a bf16 logit without
+// the Newton step (the reciprocal is good to a unit of 2^-23).
+__device__ __forceinline__ float write_strength(float b, float) {
+    float s, c;
+    sigmoid_pair<float>(-b, s, c);
+    return s;
+}
+__device__ __forceinline__ float write_strength(float b, __bf16) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(b * -0x1.715476p+0f));
+}
+
 // Gates of one element from what the caller passes: the decay, its complement
 // and the write strength (tied: the complement).
-template <bool TIED, bool LOGITS>
+template <typename DT, bool TIED, bool LOGITS>
 __device__ __forceinline__ void gates(float a, float b, float &alpha, float &keep, float &beta) {
     if constexpr (LOGITS) {
-        sigmoid_pair(a, alpha, keep);
-        if constexpr (!TIED) {
-            float unused;
-            sigmoid_pair(-b, beta, unused);
-        }
+        sigmoid_pair<DT>(a, alpha, keep);
+        if constexpr (!TIED) beta = write_strength(b, DT());
     } else {
         alpha = a;
         keep = 1.f - a;
@@ -135,6 +149,99 @@ __device__ __forceinline__ int64_t scan_block_ending(const ScanParams &p, int64_
     const uint32_t units = (uint32_t)(t >> 6), per = (uint32_t)(p.prefix_len >> 6);
     const uint32_t i = units / per;
     return i * per == units ? (int64_t)i - 1 : -1;
+}
+
+// Tiles of one sequence side by side (SPLIT kernels)
+//
+// A workgroup takes one tile. It publishes what the tile does to a state (A
+// and H of every channel) as soon as it knows it, finds the state in front of
+// it from what the tiles in front have published, and publishes the state
+// behind it. Every published state is A * (state in front) + H, formed the
+// same way by whoever forms it, so the result does not depend on how far a
+// workgroup had to look.
+//
+// A value and its presence travel in one word (all bits set: not there yet;
+// the launch's first kernel sets them), written and read by relaxed atomics of
+// device scope, so no fence orders them.
+//
+// Workgroups take the tiles of a chain in order from a counter. A tile waits
+// only for tiles of its chain that were taken before it, by workgroups that run
+// already and in turn wait only for earlier ones, and every taken tile
+// publishes: every wait ends.
+struct ScanSplit {
+    uint32_t *ticket;  // [chains]
+    uint64_t *agg;     // [slots][width]: A low, H high
+    uint32_t *inc;     // [slots][width]
+    int32_t chains;    // dense: N * column blocks, packed: column blocks
+    int32_t slots;     // dense: tiles * N (tile-major), packed: floor(total / tile) + N
+    int32_t width;     // columns, up to whole column blocks
+};
+
+constexpr uint32_t kAbsent = 0xFFFFFFFFu;
+
+// A value's bits; any NaN becomes the plain one, never kAbsent.
+__device__ __forceinline__ uint32_t scan_word(float x) {
+    return x == x ? __builtin_bit_cast(uint32_t, x) : 0x7FC00000u;
+}
+template <typename T> __device__ __forceinline__ void publish(T *p, T v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename T> __device__ __forceinline__ T observe(const T *p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t scan_pair(float A, float H) {
+    return (uint64_t)scan_word(H) << 32 | scan_word(A);
+}
+
+// The state in front of a tile: `ahead` tiles of its sequence lie in front, at
+// slots `at`, at + step, ... (step is negative for the backward pass's order).
+// kDeep of them are read at a time.
+__device__ __forceinline__ float scan_look(const ScanSplit &sp, int64_t at, int64_t step,
+                                           int32_t ahead, int col) {
+    constexpr int kDeep = 4;
+    for (;;) {
+        uint32_t inc[kDeep];
+        uint64_t agg[kDeep];
+#pragma unroll
+        for (int j = 0; j < kDeep; ++j) {
+            const int64_t i = (at + (j < ahead ? j : ahead - 1) * step) * sp.width + col;
+            inc[j] = observe(sp.inc + i);
+            agg[j] = observe(sp.agg + i);
+        }
+        float c = 0.f;
+        bool found = false;
+#pragma unroll
+        for (int j = kDeep - 1; j >= 0; --j) {
+            if (j >= ahead) continue;
+            if (inc[j] != kAbsent) {
+                c = __builtin_bit_cast(float, inc[j]);
+                found = true;
+            } else {
+                found &= agg[j] != ~(uint64_t)0;
+                c = fmaf(__builtin_bit_cast(float, (uint32_t)agg[j]), c,
+                         __builtin_bit_cast(float, (uint32_t)(agg[j] >> 32)));
+            }
+        }
+        if (found) return c;
+        __builtin_amdgcn_s_sleep(1);
+    }
+}
+
+// Which tile a packed batch's slot is: sequence n owns the slots from
+// floor(start / tile) + n on, as many as it has tiles, and at least one (a
+// sequence without tokens has its state handed on there).
+__device__ __forceinline__ int scan_slot_sequence(const ScanParams &p, int64_t slot) {
+    int lo = 0, hi = p.N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        int64_t base = p.cu[mid];
+        base = base < 0 ? 0 : (base > p.total ? p.total : base);
+        if (base / GDN_SCAN_TILE + mid <= slot)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
 }
 
 }  // namespace gdn
