@@ -10,12 +10,13 @@
 // left by their score in fp64. The logits are read once: bound by HBM for
 // large batches, by latency for one sequence.
 //
-// The best W of a piece: every thread keeps its best (value, place); the W-th
-// best of those is a bound that at least W elements reach and that at most W
-// threads have anything above of, so the elements that reach it are few and
-// fit a fixed buffer; they are ranked against each other. Keys hold the place
-// too, so they all differ, and neither ties nor the order of the buffer's
-// filling change the result.
+// The best W of a piece: every lane keeps its best value; the W-th best of a
+// wave's 64 (found bit by bit with ballots), and the largest of those over the
+// waves, is a bound that at least W elements reach and few others do. They are
+// collected and ranked against each other by value and place, so that neither
+// ties nor the order of the collection change the result. Where too many reach
+// the bound (rows of equal values, or of hardly anything but -inf) W rounds
+// that each find the next best take its place.
 #include "gdn_device.hpp"
 #include "gdn_ops_launch.hpp"
 
@@ -23,10 +24,9 @@ namespace gdn {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kPiece = 8192;                 // logits per workgroup
-constexpr int kPer = kPiece / kThreads;      // per thread
+constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kMaxW = 32;
+constexpr int kList = 512;  // collected elements, at the most
 constexpr float kLog2e = 0x1.715476p+0f;
 
 // A value's bits in an order of unsigned integers, -0 as +0.
@@ -58,8 +58,6 @@ struct PieceSum {
     float m, sum;  // sum of e^(l - m) over the piece; m NaN: a NaN or +inf was there
 };
 
-__host__ __device__ inline int64_t pieces_of(int64_t V) { return (V + kPiece - 1) / kPiece; }
-
 // 8 logits from any element on: rows of an odd V start off 16 bytes, and a
 // thread's share is counted from its row's start all the same, so that equal
 // rows give equal sums bit by bit and their candidates tie.
@@ -67,14 +65,26 @@ template <typename DT> struct __attribute__((packed, aligned(sizeof(DT)))) Eight
     DT v[8];
 };
 
-template <typename DT>
-__global__ __launch_bounds__(kThreads) void beam_piece_kernel(const DT *logits, int64_t V,
-                                                              int W, int npieces,
-                                                              PieceSum *sums, uint64_t *best) {
-    __shared__ uint64_t s_key[kThreads];
-    __shared__ uint64_t s_list[kMaxW * kPer];
-    __shared__ float s_red[2][4];
-    __shared__ uint64_t s_bound;
+// The largest o such that at least `want` of the wave's lanes hold x >= o (0 if
+// there is none), looked for from bit 31 down to bit `low`: bits below stay 0.
+__device__ __forceinline__ uint32_t wave_bound(uint32_t x, int want, int low) {
+    uint32_t o = 0;
+    for (int bit = 31; bit >= low; --bit) {
+        const uint32_t c = o | (1u << bit);
+        if (__popcll(__ballot(x >= c)) >= want) o = c;
+    }
+    return o;
+}
+
+// Logits per workgroup: VECS times 8 per thread.
+template <typename DT, int VECS>
+__global__ __launch_bounds__(kThreads) void beam_piece_kernel(const DT *logits, int64_t V, int W,
+                                                              int npieces, PieceSum *sums,
+                                                              uint64_t *best) {
+    constexpr int kPiece = VECS * 8 * kThreads;
+    __shared__ uint64_t s_list[kList];
+    __shared__ float s_top[kWaves], s_sum[kWaves];
+    __shared__ uint32_t s_bound[kWaves];
     __shared__ int s_count;
 
     const int64_t row = blockIdx.x / npieces;
@@ -86,11 +96,10 @@ __global__ __launch_bounds__(kThreads) void beam_piece_kernel(const DT *logits, 
     if (tid == 0) s_count = 0;
 
     // element e of vector j: the piece's (j * 256 + tid) * 8 + e
-    float v[kPer / 8][8];
+    float v[VECS][8], vtop[VECS];
     float top = -__builtin_inff();
-    bool bad = false;
 #pragma unroll
-    for (int j = 0; j < kPer / 8; ++j) {
+    for (int j = 0; j < VECS; ++j) {
         const int at = (j * kThreads + tid) * 8;
         if (at + 8 <= here) {
             const Eight<DT> q = *reinterpret_cast<const Eight<DT> *>(from + at);
@@ -101,87 +110,113 @@ __global__ __launch_bounds__(kThreads) void beam_piece_kernel(const DT *logits, 
             for (int e = 0; e < 8; ++e)
                 v[j][e] = at + e < here ? to_f32(from[at + e]) : -__builtin_inff();
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            bad |= !(v[j][e] < __builtin_inff());  // NaN or +inf: the row is dead
-            if (v[j][e] != v[j][e]) v[j][e] = -__builtin_inff();
-            top = fmaxf(top, v[j][e]);
-        }
     }
-    top = wave_max(top);
-    const uint64_t anybad = __ballot(bad);
-    if (lane == 0) s_red[0][wave] = anybad ? __builtin_nanf("") : top;
+#pragma unroll
+    for (int j = 0; j < VECS; ++j) {
+        vtop[j] = -__builtin_inff();  // a NaN is passed over here and found in the sum
+#pragma unroll
+        for (int e = 0; e < 8; ++e) vtop[j] = fmaxf(vtop[j], v[j][e]);
+        top = fmaxf(top, vtop[j]);
+    }
+    // bf16 values differ in their upper 16 bits only
+    const uint32_t wb = wave_bound(ordered(top), W, sizeof(DT) == 2 ? 16 : 0);
+    const float wt = wave_max(top);
+    if (lane == 0) {
+        s_top[wave] = wt;
+        s_bound[wave] = wb;
+    }
     __syncthreads();
-    float m = -__builtin_inff();
-    bool dead = false;
+    float m = s_top[0];
+    uint32_t ob = s_bound[0];
 #pragma unroll
-    for (int i = 0; i < kThreads / 64; ++i) {
-        dead |= s_red[0][i] != s_red[0][i];
-        m = fmaxf(m, s_red[0][i]);
+    for (int i = 1; i < kWaves; ++i) {
+        m = fmaxf(m, s_top[i]);
+        ob = max(ob, s_bound[i]);
     }
-    // l - m first: the terms that count are near 0 there, so that no rounding is
-    // common to all of them, and the lowest finite values neither overflow nor
-    // drop out of a row that holds nothing else
+    uint64_t *out = best + (int64_t)blockIdx.x * W;
+    const bool some = m > -__builtin_inff();
+    // The sum of e^(l - m): l - m first, for the terms that count are near 0
+    // there, so that no rounding is common to all of them, and the lowest finite
+    // values neither overflow nor drop out of a row that holds nothing else. A
+    // NaN makes it NaN, and so does +inf, which is m then.
     float sum = 0.f;
-    if (m > -__builtin_inff()) {
+    if (some) {
 #pragma unroll
-        for (int j = 0; j < kPer / 8; ++j)
+        for (int j = 0; j < VECS; ++j)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                sum += __builtin_amdgcn_exp2f((v[j][e] - m) * kLog2e);  // -inf: 0
-            }
+            for (int e = 0; e < 8; ++e)
+                sum += __builtin_amdgcn_exp2f((v[j][e] - m) * kLog2e);
+    } else {
+#pragma unroll
+        for (int j = 0; j < VECS; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (v[j][e] != v[j][e]) sum = v[j][e];
     }
     sum = wave_sum(sum);
+    if (lane == 0) s_sum[wave] = sum;
 
-    // the thread's best; places rise with j and e, so the first of equals stays
-    float bv = 0.f;
-    int bp = -1;
+    // A bf16 bound has the lower half of its bits clear, which is the lowest
+    // of the (negative) or the only (positive) pattern with that upper half.
+    const float bound = unordered(ob);
+    const bool picky = some && ob > ordered(-__builtin_inff());
+    if (picky && top >= bound) {
 #pragma unroll
-    for (int j = 0; j < kPer / 8; ++j)
+        for (int j = 0; j < VECS; ++j) {
+            if (!(vtop[j] >= bound)) continue;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int at = (j * kThreads + tid) * 8 + e;
-            if (at < here && (bp < 0 || v[j][e] > bv)) {
-                bv = v[j][e];
-                bp = at;
-            }
-        }
-    // a thread without elements: a key below all real ones, its own
-    const uint64_t mine = bp < 0 ? (uint64_t)tid : key_of(bv, first + bp);
-    s_key[tid] = mine;
-    if (lane == 0) s_red[1][wave] = sum;
-    __syncthreads();
-    int above = 0;
-    for (int i = 0; i < kThreads; ++i) above += s_key[i] > mine;
-    if (above == W - 1) s_bound = mine;
-    __syncthreads();
-    const uint64_t bound = s_bound;
-    if (mine >= bound && bp >= 0) {
-#pragma unroll
-        for (int j = 0; j < kPer / 8; ++j)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int at = (j * kThreads + tid) * 8 + e;
-                if (at < here) {
-                    const uint64_t k = key_of(v[j][e], first + at);
-                    if (k >= bound) s_list[atomicAdd(&s_count, 1)] = k;
+            for (int e = 0; e < 8; ++e)
+                if (v[j][e] >= bound) {  // elements past the end are -inf
+                    const int i = atomicAdd(&s_count, 1);
+                    if (i < kList)
+                        s_list[i] = key_of(v[j][e], first + (j * kThreads + tid) * 8 + e);
                 }
-            }
+        }
     }
     __syncthreads();
-    const int count = s_count;
-    uint64_t *out = best + (int64_t)blockIdx.x * W;
-    for (int i = tid; i < count; i += kThreads) {
-        const uint64_t k = s_list[i];
-        int rank = 0;
-        for (int q = 0; q < count; ++q) rank += s_list[q] > k;
-        if (rank < W) out[rank] = k;
-    }
-    if (tid >= count && tid < W) out[tid] = 0;  // fewer elements than W
     if (tid == 0) {
-        float all = 0.f;
-        for (int i = 0; i < kThreads / 64; ++i) all += s_red[1][i];
-        sums[blockIdx.x] = PieceSum{dead ? __builtin_nanf("") : m, all};
+        float all = s_sum[0];
+#pragma unroll
+        for (int i = 1; i < kWaves; ++i) all += s_sum[i];
+        sums[blockIdx.x] = PieceSum{all != all ? all : m, all};
+    }
+    const int count = s_count;
+    if (picky && count <= kList) {
+        for (int i = tid; i < count; i += kThreads) {
+            const uint64_t k = s_list[i];
+            int rank = 0;
+            for (int q = 0; q < count; ++q) rank += s_list[q] > k;
+            if (rank < W) out[rank] = k;
+        }
+        if (tid >= count && tid < W) out[tid] = 0;
+    } else if (!some) {
+        if (tid < W) out[tid] = tid < here ? key_of(-__builtin_inff(), first + tid) : 0;
+    } else {  // W rounds, each the best key below the last one
+        uint64_t last = ~(uint64_t)0;
+        for (int k = 0; k < W; ++k) {
+            uint64_t c = 0;
+#pragma unroll
+            for (int j = 0; j < VECS; ++j)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int at = (j * kThreads + tid) * 8 + e;
+                    const uint64_t x = key_of(v[j][e], first + at);
+                    if (at < here && v[j][e] == v[j][e] && x < last && x > c) c = x;
+                }
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const uint64_t x = __shfl_xor(c, o);
+                c = x > c ? x : c;
+            }
+            __syncthreads();  // the list and the round in front are read
+            if (lane == 0) s_list[wave] = c;
+            __syncthreads();
+            c = s_list[0];
+#pragma unroll
+            for (int i = 1; i < kWaves; ++i) c = s_list[i] > c ? s_list[i] : c;
+            if (tid == 0) out[k] = c;  // 0: none left
+            last = c;
+        }
     }
 }
 
@@ -207,20 +242,66 @@ __device__ __forceinline__ Cand wave_best(Cand c) {
     return c;
 }
 
-// One workgroup per batch item: the logsumexp of its beams, then W rounds that
-// each take the best candidate behind the last one taken.
-__global__ __launch_bounds__(kThreads) void beam_join_kernel(BeamParams p, int npieces,
-                                                             const PieceSum *sums,
-                                                             const uint64_t *best) {
-    __shared__ double s_logsum[kMaxW];  // log of the sum of e^(l - m)
-    __shared__ float s_m[kMaxW];
-    __shared__ float s_score[kMaxW];
-    __shared__ int s_done[kMaxW], s_live[kMaxW];
-    __shared__ Cand s_pick[kThreads / 64];
+// What a beam offers, by the join kernel's shared arrays.
+struct BeamRow {
+    double logsum;  // log of the sum of e^(l - m)
+    float m, score;
+    int done, live;
+};
+
+// Candidate q of beam w (of npieces * W): a piece's key, or what a beam that
+// has ended or is dead offers in its place.
+__device__ __forceinline__ Cand candidate(const BeamRow &r, int w, int q, int W, int64_t V,
+                                          int32_t eos, uint64_t key) {
+    Cand d{-__builtin_inf(), -1};
+    if (!r.live) {  // its tokens in order at -inf
+        if (q < W && q < V) d.place = w * V + q;
+    } else if (r.done) {  // itself, then its other tokens in order at -inf
+        const int64_t v = q == 0 ? eos : (q - 1 < eos ? q - 1 : q);
+        if (q == 0) d.score = r.score;
+        if (q < W && v < V) d.place = w * V + v;
+    } else if (key >> 32) {
+        const float l = unordered((uint32_t)(key >> 32));
+        d.score = (double)r.score + (((double)l - (double)r.m) - r.logsum);
+        d.place = w * V + (uint32_t)~(uint32_t)key;
+    }
+    return d;
+}
+
+// A score in 32 ordered bits, rounded down: a >= b keeps its order or ties.
+// 0 for no candidate.
+__device__ __forceinline__ uint32_t score_bits(const Cand &c) {
+    return c.place < 0 ? 0u : ordered(__double2float_rd(c.score));
+}
+
+// One workgroup per batch item: the logsumexp of its beams, then the W best of
+// the pieces' candidates, found as in a piece (a bound from the scores rounded
+// down to 32 bits, then a ranking in fp64).
+// A thread holds up to HELD candidates; where there are more, all is done by
+// rounds.
+template <int THREADS, int HELD>
+__global__ __launch_bounds__(THREADS) void beam_join_kernel(BeamParams p, int npieces,
+                                                            const PieceSum *sums,
+                                                            const uint64_t *best) {
+    constexpr int kWaves = THREADS / 64;
+    __shared__ BeamRow s_row[kMaxW];
+    __shared__ Cand s_list[kList];
+    __shared__ uint32_t s_bound[kWaves];
+    __shared__ int s_count;
 
     const int b = blockIdx.x, W = p.W, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t V = p.V;
-    for (int w = wave; w < W; w += kThreads / 64) {
+    const int per = npieces * W, n = W * per;  // candidates of a beam, and all
+    const uint64_t *keys = best + (int64_t)b * n;
+    const bool held = n <= HELD * THREADS;
+    uint64_t key[HELD];
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) {
+        const int i = j * THREADS + tid;
+        key[j] = held && i < n ? keys[i] : 0;
+    }
+    if (tid == 0) s_count = 0;
+    for (int w = wave; w < W; w += kWaves) {
         const int64_t row = (int64_t)b * W + w;
         const PieceSum *ps = sums + row * npieces;
         float m = -__builtin_inff();
@@ -243,59 +324,79 @@ __global__ __launch_bounds__(kThreads) void beam_join_kernel(BeamParams p, int n
             const bool done = p.finished && p.finished[row];
             const bool live = fabsf(s) < __builtin_inff() &&
                               (done || (!nan && m > -__builtin_inff()));
-            s_m[w] = m;
-            s_logsum[w] = live && !done ? log(sum) : 0.0;
-            s_score[w] = s;
-            s_done[w] = done;
-            s_live[w] = live;
+            s_row[w] = BeamRow{live && !done ? log(sum) : 0.0, m, s, done, live};
         }
     }
     __syncthreads();
 
-    const int per = npieces * W;  // candidates of a beam
-    Cand last{__builtin_inf(), -1};
-    bool any = false;
+    const auto write = [&](int k, const Cand &c) {
+        const int w = (int)(c.place / V);
+        const int32_t v = (int32_t)(c.place - w * V);
+        const int64_t to = (int64_t)b * W + k;
+        p.new_scores[to] = (float)c.score;
+        p.tokens[to] = v;
+        p.parents[to] = w;
+        if (p.new_finished) p.new_finished[to] = s_row[w].done || v == p.eos;
+        if (p.src_slots) p.src_slots[to] = p.slots[(int64_t)b * W + w];
+    };
+
+    if (held) {
+        Cand c[HELD];
+        uint32_t bits[HELD], top = 0;
+#pragma unroll
+        for (int j = 0; j < HELD; ++j) {
+            const int i = j * THREADS + tid;
+            c[j].place = -1;
+            if (i < n) {
+                const int w = i / per;
+                c[j] = candidate(s_row[w], w, i - w * per, W, V, p.eos, key[j]);
+            }
+            bits[j] = score_bits(c[j]);
+            top = max(top, bits[j]);
+        }
+        const uint32_t wb = wave_bound(top, W, 0);
+        if (lane == 0) s_bound[wave] = wb;
+        __syncthreads();
+        uint32_t bound = s_bound[0];
+#pragma unroll
+        for (int i = 1; i < kWaves; ++i) bound = max(bound, s_bound[i]);
+#pragma unroll
+        for (int j = 0; j < HELD; ++j)
+            if (c[j].place >= 0 && bits[j] >= bound) {
+                const int i = atomicAdd(&s_count, 1);
+                if (i < kList) s_list[i] = c[j];
+            }
+        __syncthreads();
+        const int count = s_count;
+        if (count <= kList) {  // at least W: every beam offers min(W, V)
+            for (int i = tid; i < count; i += THREADS) {
+                const Cand x = s_list[i];
+                int rank = 0;
+                for (int q = 0; q < count; ++q) rank += before(s_list[q], x);
+                if (rank < W) write(rank, x);
+            }
+            return;
+        }
+    }
+
+    // W rounds, each the best candidate behind the last one taken
+    Cand last{0.0, -1};
     for (int k = 0; k < W; ++k) {
         Cand c{0.0, -1};
-        for (int i = tid; i < W * per; i += kThreads) {
-            const int w = i / per, q = i - w * per;
-            const int64_t row = (int64_t)b * W + w;
-            Cand d{-__builtin_inf(), -1};
-            if (!s_live[w]) {  // its tokens in order at -inf
-                if (q < W && q < V) d.place = w * V + q;
-            } else if (s_done[w]) {  // itself, then its other tokens in order at -inf
-                const int64_t v = q == 0 ? p.eos : (q - 1 < p.eos ? q - 1 : q);
-                if (q == 0) d.score = s_score[w];
-                if (q < W && v < V) d.place = w * V + v;
-            } else {
-                const uint64_t key = best[row * per + q];
-                if (key >> 32) {
-                    const float l = unordered((uint32_t)(key >> 32));
-                    d.score = (double)s_score[w] + (((double)l - (double)s_m[w]) - s_logsum[w]);
-                    d.place = w * V + (uint32_t)~(uint32_t)key;
-                }
-            }
-            if (d.place >= 0 && (!any || before(last, d))) c = better(c, d);
+        for (int i = tid; i < n; i += THREADS) {
+            const int w = i / per;
+            const Cand d = candidate(s_row[w], w, i - w * per, W, V, p.eos, keys[i]);
+            if (d.place >= 0 && (k == 0 || before(last, d))) c = better(c, d);
         }
         c = wave_best(c);
-        if (lane == 0) s_pick[wave] = c;
+        __syncthreads();  // the round in front is read
+        if (lane == 0) s_list[wave] = c;
         __syncthreads();
-        c = s_pick[0];
+        c = s_list[0];
 #pragma unroll
-        for (int i = 1; i < kThreads / 64; ++i) c = better(c, s_pick[i]);
+        for (int i = 1; i < kWaves; ++i) c = better(c, s_list[i]);
         last = c;
-        any = true;
-        if (tid == 0) {
-            const int w = (int)(c.place / V);
-            const int32_t v = (int32_t)(c.place - w * V);
-            const int64_t to = (int64_t)b * W + k;
-            p.new_scores[to] = (float)c.score;
-            p.tokens[to] = v;
-            p.parents[to] = w;
-            if (p.new_finished) p.new_finished[to] = s_done[w] || v == p.eos;
-            if (p.src_slots) p.src_slots[to] = p.slots[(int64_t)b * W + w];
-        }
-        __syncthreads();
+        if (tid == 0) write(k, c);
     }
 }
 
@@ -322,31 +423,52 @@ __global__ __launch_bounds__(256) void gather_kernel(const u32x4 *src, int64_t n
     }
 }
 
+// 8 logits per thread where a piece of 32 per thread would leave CUs without a
+// workgroup, else 32.
+int piece_vecs(int64_t rows, int64_t V) {
+    return rows * ((V + 8191) / 8192) < 256 ? 1 : 4;
+}
+
+int64_t pieces_of(int64_t rows, int64_t V) {
+    const int64_t piece = piece_vecs(rows, V) * 8 * kThreads;
+    return (V + piece - 1) / piece;
+}
+
 size_t keys_offset(int64_t pieces) { return ((size_t)pieces * sizeof(PieceSum) + 255) / 256 * 256; }
 
 }  // namespace
 
 size_t beam_workspace_bytes(int32_t B, int32_t W, int64_t V, int) {
-    const int64_t pieces = (int64_t)B * W * pieces_of(V);
+    const int64_t rows = (int64_t)B * W, pieces = rows * pieces_of(rows, V);
     return keys_offset(pieces) + (size_t)pieces * W * 8;
 }
 
 hipError_t launch_beam(const BeamParams &p, int dtype, void *ws, hipStream_t stream) {
-    const int64_t np = pieces_of(p.V), pieces = (int64_t)p.B * p.W * np;
+    const int64_t rows = (int64_t)p.B * p.W, np = pieces_of(rows, p.V), pieces = rows * np;
     PieceSum *sums = static_cast<PieceSum *>(ws);
     uint64_t *best = reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + keys_offset(pieces));
-    if (dtype == 1)
-        hipLaunchKernelGGL(beam_piece_kernel<__bf16>, dim3((unsigned)pieces), dim3(kThreads), 0,
-                           stream, static_cast<const __bf16 *>(p.logits), p.V, p.W, (int)np, sums,
-                           best);
-    else
-        hipLaunchKernelGGL(beam_piece_kernel<float>, dim3((unsigned)pieces), dim3(kThreads), 0,
-                           stream, static_cast<const float *>(p.logits), p.V, p.W, (int)np, sums,
-                           best);
+    const bool few = piece_vecs(rows, p.V) == 1;
+#define GDN_BEAM_LAUNCH(DT, VECS)                                                                    hipLaunchKernelGGL((beam_piece_kernel<DT, VECS>), dim3((unsigned)pieces), dim3(kThreads), 0,                        stream, static_cast<const DT *>(p.logits), p.V, p.W, (int)np, sums, best)
+    if (dtype == 1) {
+        if (few)
+            GDN_BEAM_LAUNCH(__bf16, 1);
+        else
+            GDN_BEAM_LAUNCH(__bf16, 4);
+    } else {
+        if (few)
+            GDN_BEAM_LAUNCH(float, 1);
+        else
+            GDN_BEAM_LAUNCH(float, 4);
+    }
+#undef GDN_BEAM_LAUNCH
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(beam_join_kernel, dim3((unsigned)p.B), dim3(kThreads), 0, stream, p,
-                       (int)np, sums, best);
+    if (np * p.W * p.W <= 1024)
+        hipLaunchKernelGGL((beam_join_kernel<256, 4>), dim3((unsigned)p.B), dim3(256), 0, stream,
+                           p, (int)np, sums, best);
+    else
+        hipLaunchKernelGGL((beam_join_kernel<1024, 8>), dim3((unsigned)p.B), dim3(1024), 0,
+                           stream, p, (int)np, sums, best);
     return hipGetLastError();
 }
 
