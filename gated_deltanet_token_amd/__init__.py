@@ -17,6 +17,7 @@ the kernels: raw q/k rows are L2-normalised, alpha/beta are given as logits.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -363,44 +364,62 @@ def gdn_decode_multi(q, k, v, alpha, beta, state_pool, src_slot, dst_slot, *, ou
     return out, step_states
 
 
-class _On:
-    """Device and stream of one call: torch allocates and the library launches
-    there, whatever the current device and stream are."""
-
-    def __init__(self, dev, stream):
-        if dev.type != "cuda":
-            raise ValueError(f"tensors must be on a GPU, got {dev}")
-        self.stream = stream if stream is not None else torch.cuda.current_stream(dev)
-        self._outer = None
-        if stream is not None or torch.cuda.current_device() != dev.index:
-            self._outer = torch.cuda.stream(self.stream)
-
-    def __enter__(self):
-        if self._outer is not None:
-            self._outer.__enter__()
-        return self.stream.cuda_stream
-
-    def __exit__(self, *exc):
-        if self._outer is not None:
-            self._outer.__exit__(*exc)
-
-
-def _dims(t, name, n):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != n:
-        raise ValueError(f"{name} must have {n} dimensions, got shape {tuple(t.shape)}")
-    return t.shape
+def _on_stream(first):
+    """Runs a call on the device of its argument `first` and on its `stream`
+    argument: torch allocates and the library launches there, whatever the
+    current device and stream are."""
+    def wrap(fn):
+        @functools.wraps(fn)
+        def call(*args, stream=None, **kw):
+            t = args[0] if args else kw.get(first)
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{first} must be a torch.Tensor")
+            index = t.get_device()
+            if index < 0:
+                return fn(*args, **kw)  # refused there
+            if stream is None:
+                if torch._C._cuda_getDevice() == index:
+                    return fn(*args, **kw)
+                stream = torch.cuda.current_stream(index)
+            elif stream.device_index != index:
+                raise ValueError(f"stream is on device {stream.device_index}, {first} on {index}")
+            with torch.cuda.stream(stream):
+                return fn(*args, **kw)
+        return call
+    return wrap
 
 
-def _opt(t, name, dtype, shape, device):
-    if t is not None:
-        _need(t, name, dtype, shape, device)
+def _raw_stream(index):
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
-def _scratch(workspace, size, dev, stream):
+def _like(t, name, dtype, shape, index):
+    """_need with the checks that nearly always pass first: these calls are made
+    once per token and layer."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == index and t.is_contiguous()):
+        _need(t, name, dtype, shape, torch.device("cuda", index) if index >= 0 else None)
+        raise ValueError(f"{name} is not as required")
+
+
+def _on_gpu(index):
+    if index < 0:
+        raise ValueError("tensors must be on a GPU")
+
+
+def _start(t, name, dims):
+    """Type code, device index and shape of a call's first tensor."""
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return _dtype_code(t), t.get_device(), t.shape
+
+
+def _scratch(workspace, size, index, like):
     """(pointer, bytes, keep-alive) of a workspace argument whose size the
-    library names through size(): None, "auto" or a tensor."""
+    library names through size(): None, "auto" or a tensor. Allocated in the
+    element type of `like`, a tensor of the call (the quickest way to allocate)."""
     if workspace is None:
         return None, 0, None
     if isinstance(workspace, str):
@@ -409,10 +428,10 @@ def _scratch(workspace, size, dev, stream):
         n = size()
         if n == 0:
             return None, 0, None
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        workspace = like.new_empty((n + 3) // like.element_size())
         return workspace.data_ptr(), n, workspace
-    _need(workspace, "workspace", device=dev)
-    workspace.record_stream(stream)
+    _need(workspace, "workspace", device=torch.device("cuda", index))
+    workspace.record_stream(torch.cuda.current_stream(index))
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
@@ -423,270 +442,295 @@ def gdn_scan_workspace_size(num_seqs, tokens, D, dtype, packed) -> int:
                                                       int(bool(packed))))
 
 
-def _scan_forward(x, alpha, beta, cu, h0, out, final, want_final, prefix, interval, flags,
-                  workspace, stream):
-    lib = load_library()
-    code = _dtype_code(x)
-    dev, D = x.device, x.shape[-1]
-    packed = cu is not None
-    _need(x, "x")
-    _need(alpha, "alpha", x.dtype, x.shape, dev)
-    _opt(beta, "beta", x.dtype, x.shape, dev)
-    if packed:
-        _need(cu, "cu_seqlens", torch.int32, device=dev)
-        n, tokens = _dims(cu, "cu_seqlens", 1)[0] - 1, x.shape[0]
-    else:
-        n, tokens = x.shape[0], x.shape[1]
-    _opt(h0, "initial_state", torch.float32, (n, D), dev)
-    _opt(out, "out", x.dtype, x.shape, dev)
-    _opt(final, "final_state", torch.float32, (n, D), dev)
+def _scan_sizes(x, cu, index):
+    """(sequences, tokens of one or of the batch, channels)."""
+    if cu is None:
+        return x.shape
+    if not isinstance(cu, torch.Tensor) or cu.dim() != 1:
+        raise ValueError("cu_seqlens must be a one-dimensional tensor")
+    _like(cu, "cu_seqlens", torch.int32, cu.shape, index)
+    return cu.shape[0] - 1, x.shape[0], x.shape[1]
+
+
+def _scan_prefix(prefix, interval, n, tokens, packed, D, index):
     interval = int(interval)
     if prefix is not None:
         if interval < 1:
             raise ValueError("prefix_interval must be >= 1 with prefix_states")
-        _need(prefix, "prefix_states", torch.float32,
-              (prefix_state_rows(n, tokens, interval, packed), D), dev)
-    on = _On(dev, stream)
-    with on as st:
-        if out is None:
-            out = torch.empty_like(x)
-        if final is None and want_final:
-            final = torch.empty((n, D), dtype=torch.float32, device=dev)
-        wp, wb, _keep = _scratch(
-            workspace, lambda: lib.gdn_scan_workspace_size(n, tokens, D, code, int(packed)), dev,
-            on.stream)
-        if packed:
-            rc = lib.gdn_scan_varlen_prefill(
-                x.data_ptr(), alpha.data_ptr(), _ptr(beta), cu.data_ptr(), n, tokens, _ptr(h0),
-                out.data_ptr(), _ptr(final), _ptr(prefix), interval, D, code, flags, wp, wb, st)
-        else:
-            rc = lib.gdn_scan_prefill(
-                x.data_ptr(), alpha.data_ptr(), _ptr(beta), _ptr(h0), out.data_ptr(), _ptr(final),
-                _ptr(prefix), interval, n, tokens, D, code, flags, wp, wb, st)
-    _check(rc)
+        _like(prefix, "prefix_states", torch.float32,
+              (prefix_state_rows(n, tokens, interval, packed), D), index)
+    return interval
+
+
+def _scan_forward(x, alpha, beta, cu, h0, out, final, want_final, prefix, interval, flags,
+                  workspace):
+    lib = _lib or load_library()
+    packed = cu is not None
+    code, index, shape = _start(x, "x", 2 if packed else 3)
+    dt = x.dtype
+    _like(alpha, "alpha", dt, shape, index)
+    if beta is not None:
+        _like(beta, "beta", dt, shape, index)
+    n, tokens, D = _scan_sizes(x, cu, index)
+    if h0 is not None:
+        _like(h0, "initial_state", torch.float32, (n, D), index)
+    interval = _scan_prefix(prefix, interval, n, tokens, packed, D, index)
+    _on_gpu(index)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _like(out, "out", dt, shape, index)
+    if final is not None:
+        _like(final, "final_state", torch.float32, (n, D), index)
+    elif want_final:
+        final = torch.empty_like(h0) if h0 is not None else x.new_empty((n, D), dtype=torch.float32)
+    wp, wb, _keep = _scratch(
+        workspace, lambda: lib.gdn_scan_workspace_size(n, tokens, D, code, int(packed)), index,
+        x)
+    if packed:
+        rc = lib.gdn_scan_varlen_prefill(
+            x.data_ptr(), alpha.data_ptr(), _ptr(beta), cu.data_ptr(), n, tokens, _ptr(h0),
+            out.data_ptr(), _ptr(final), _ptr(prefix), interval, D, code, flags, wp, wb,
+            _raw_stream(index))
+    else:
+        rc = lib.gdn_scan_prefill(
+            x.data_ptr(), alpha.data_ptr(), _ptr(beta), _ptr(h0), out.data_ptr(), _ptr(final),
+            _ptr(prefix), interval, n, tokens, D, code, flags, wp, wb, _raw_stream(index))
+    if rc:
+        _check(rc)
     return out, final
 
 
+@_on_stream("x")
 def gdn_scan_prefill(x, alpha, beta=None, initial_state=None, *, out=None, final_state=None,
                      want_final_state: bool = True, prefix_states=None, prefix_interval: int = 0,
-                     flags: int = 0, workspace="auto", stream=None):
+                     flags: int = 0, workspace="auto"):
     """Gated linear recurrence h_t = alpha_t h_{t-1} + beta_t x_t per channel.
     x, alpha, beta [B,T,D] of one dtype (beta None: 1 - alpha); initial_state
     [B,D] fp32 or None. Returns (out [B,T,D], final_state [B,D] fp32).
     prefix_states: optional fp32 [prefix_state_rows(B, T, interval, False), D]
     receiving the state after every whole block of 64 * prefix_interval tokens
-    (gdn_scan_backward takes them with an interval of 1 or 2)."""
-    _dims(x, "x", 3)
+    (gdn_scan_backward takes them with an interval of 1 or 2). `stream` (a
+    torch.cuda.Stream, here and in the calls below): where to run, the current
+    one by default."""
     return _scan_forward(x, alpha, beta, None, initial_state, out, final_state, want_final_state,
-                         prefix_states, prefix_interval, flags, workspace, stream)
+                         prefix_states, prefix_interval, flags, workspace)
 
 
+@_on_stream("x")
 def gdn_scan_varlen_prefill(x, alpha, beta, cu_seqlens, initial_state=None, *, out=None,
                             final_state=None, want_final_state: bool = True, prefix_states=None,
-                            prefix_interval: int = 0, flags: int = 0, workspace="auto",
-                            stream=None):
+                            prefix_interval: int = 0, flags: int = 0, workspace="auto"):
     """gdn_scan_prefill over packed sequences: x, alpha, beta [total,D];
     cu_seqlens int32 [N+1] on the device; states [N,D]."""
-    _dims(x, "x", 2)
-    _dims(cu_seqlens, "cu_seqlens", 1)
+    if cu_seqlens is None:
+        raise TypeError("cu_seqlens must be a torch.Tensor")
     return _scan_forward(x, alpha, beta, cu_seqlens, initial_state, out, final_state,
-                         want_final_state, prefix_states, prefix_interval, flags, workspace,
-                         stream)
+                         want_final_state, prefix_states, prefix_interval, flags, workspace)
 
 
 def _scan_backward(dout, x, alpha, beta, cu, h0, prefix, interval, dfinal, dx, dalpha, dbeta,
-                   dinitial, want_dinitial, flags, workspace, stream):
-    lib = load_library()
-    code = _dtype_code(x)
-    dev, D = x.device, x.shape[-1]
+                   dinitial, want_dinitial, flags, workspace):
+    lib = _lib or load_library()
     packed = cu is not None
-    _need(x, "x")
-    _need(dout, "dout", x.dtype, x.shape, dev)
-    _need(alpha, "alpha", x.dtype, x.shape, dev)
-    _opt(beta, "beta", x.dtype, x.shape, dev)
-    if packed:
-        _need(cu, "cu_seqlens", torch.int32, device=dev)
-        n, tokens = _dims(cu, "cu_seqlens", 1)[0] - 1, x.shape[0]
-    else:
-        n, tokens = x.shape[0], x.shape[1]
-    _opt(h0, "initial_state", torch.float32, (n, D), dev)
-    _opt(dfinal, "dfinal", torch.float32, (n, D), dev)
-    _opt(dx, "dx", x.dtype, x.shape, dev)
-    _opt(dalpha, "dalpha", x.dtype, x.shape, dev)
-    _opt(dbeta, "dbeta", x.dtype, x.shape, dev)
-    _opt(dinitial, "dinitial", torch.float32, (n, D), dev)
-    if beta is None and dbeta is not None:
+    code, index, shape = _start(dout, "dout", 2 if packed else 3)
+    dt = dout.dtype
+    _like(x, "x", dt, shape, index)
+    _like(alpha, "alpha", dt, shape, index)
+    if beta is not None:
+        _like(beta, "beta", dt, shape, index)
+    elif dbeta is not None:
         raise ValueError("dbeta must be None with tied gates (beta None)")
-    interval = int(interval)
-    if prefix is not None:
-        if interval < 1:
-            raise ValueError("prefix_interval must be >= 1 with prefix_states")
-        _need(prefix, "prefix_states", torch.float32,
-              (prefix_state_rows(n, tokens, interval, packed), D), dev)
-    elif tokens > SCAN_TILE:
+    n, tokens, D = _scan_sizes(x, cu, index)
+    for t, name in ((h0, "initial_state"), (dfinal, "dfinal"), (dinitial, "dinitial")):
+        if t is not None:
+            _like(t, name, torch.float32, (n, D), index)
+    for t, name in ((dx, "dx"), (dalpha, "dalpha"), (dbeta, "dbeta")):
+        if t is not None:
+            _like(t, name, dt, shape, index)
+    interval = _scan_prefix(prefix, interval, n, tokens, packed, D, index)
+    if prefix is None and tokens > SCAN_TILE:
         raise ValueError(f"prefix_states are needed for more than {SCAN_TILE} tokens")
-    on = _On(dev, stream)
-    with on as st:
-        dx = torch.empty_like(x) if dx is None else dx
-        dalpha = torch.empty_like(x) if dalpha is None else dalpha
-        if beta is not None and dbeta is None:
-            dbeta = torch.empty_like(x)
-        if dinitial is None and want_dinitial:
-            dinitial = torch.empty((n, D), dtype=torch.float32, device=dev)
-        wp, wb, _keep = _scratch(
-            workspace, lambda: lib.gdn_scan_workspace_size(n, tokens, D, code, int(packed)), dev,
-            on.stream)
-        tail = (_ptr(prefix), interval, _ptr(dfinal), dx.data_ptr(), dalpha.data_ptr(),
-                _ptr(dbeta), _ptr(dinitial))
-        if packed:
-            rc = lib.gdn_scan_varlen_backward(
-                dout.data_ptr(), x.data_ptr(), alpha.data_ptr(), _ptr(beta), cu.data_ptr(), n,
-                tokens, _ptr(h0), *tail, D, code, flags, wp, wb, st)
-        else:
-            rc = lib.gdn_scan_backward(
-                dout.data_ptr(), x.data_ptr(), alpha.data_ptr(), _ptr(beta), _ptr(h0), *tail, n,
-                tokens, D, code, flags, wp, wb, st)
-    _check(rc)
+    _on_gpu(index)
+    dx = torch.empty_like(x) if dx is None else dx
+    dalpha = torch.empty_like(x) if dalpha is None else dalpha
+    if beta is not None and dbeta is None:
+        dbeta = torch.empty_like(x)
+    if dinitial is None and want_dinitial:
+        dinitial = x.new_empty((n, D), dtype=torch.float32)
+    wp, wb, _keep = _scratch(
+        workspace, lambda: lib.gdn_scan_workspace_size(n, tokens, D, code, int(packed)), index,
+        x)
+    tail = (_ptr(prefix), interval, _ptr(dfinal), dx.data_ptr(), dalpha.data_ptr(), _ptr(dbeta),
+            _ptr(dinitial))
+    if packed:
+        rc = lib.gdn_scan_varlen_backward(
+            dout.data_ptr(), x.data_ptr(), alpha.data_ptr(), _ptr(beta), cu.data_ptr(), n, tokens,
+            _ptr(h0), *tail, D, code, flags, wp, wb, _raw_stream(index))
+    else:
+        rc = lib.gdn_scan_backward(
+            dout.data_ptr(), x.data_ptr(), alpha.data_ptr(), _ptr(beta), _ptr(h0), *tail, n,
+            tokens, D, code, flags, wp, wb, _raw_stream(index))
+    if rc:
+        _check(rc)
     return dx, dalpha, dbeta, dinitial
 
 
+@_on_stream("dout")
 def gdn_scan_backward(dout, x, alpha, beta=None, initial_state=None, *, prefix_states=None,
                       prefix_interval: int = 0, dfinal=None, dx=None, dalpha=None, dbeta=None,
                       dinitial=None, want_dinitial: bool = True, flags: int = 0,
-                      workspace="auto", stream=None):
+                      workspace="auto"):
     """Gradients of gdn_scan_prefill: dout [B,T,D], dfinal [B,D] fp32 or None,
     and the forward call's inputs, with the prefix states it wrote
     (prefix_interval 1 or 2; None for T <= SCAN_TILE). Returns (dx, dalpha,
     dbeta or None, dinitial [B,D] fp32 or None); with GDN_GATE_LOGITS dalpha
     and dbeta are the logits' gradients."""
-    _dims(x, "x", 3)
     return _scan_backward(dout, x, alpha, beta, None, initial_state, prefix_states,
                           prefix_interval, dfinal, dx, dalpha, dbeta, dinitial, want_dinitial,
-                          flags, workspace, stream)
+                          flags, workspace)
 
 
+@_on_stream("dout")
 def gdn_scan_varlen_backward(dout, x, alpha, beta, cu_seqlens, initial_state=None, *,
                              prefix_states=None, prefix_interval: int = 0, dfinal=None, dx=None,
                              dalpha=None, dbeta=None, dinitial=None, want_dinitial: bool = True,
-                             flags: int = 0, workspace="auto", stream=None):
+                             flags: int = 0, workspace="auto"):
     """Gradients of gdn_scan_varlen_prefill: tensors [total,D], states [N,D]."""
-    _dims(x, "x", 2)
-    _dims(cu_seqlens, "cu_seqlens", 1)
+    if cu_seqlens is None:
+        raise TypeError("cu_seqlens must be a torch.Tensor")
     return _scan_backward(dout, x, alpha, beta, cu_seqlens, initial_state, prefix_states,
                           prefix_interval, dfinal, dx, dalpha, dbeta, dinitial, want_dinitial,
-                          flags, workspace, stream)
+                          flags, workspace)
 
 
-def gdn_scan_decode(x, alpha, beta, state_pool, src_slot, dst_slot, *, out=None, flags: int = 0,
-                    stream=None):
+@_on_stream("x")
+def gdn_scan_decode(x, alpha, beta, state_pool, src_slot, dst_slot, *, out=None, flags: int = 0):
     """K tokens of the gated linear recurrence per sequence against a pool of
     state slots. x, alpha, beta [B,K,D] (beta None: 1 - alpha); state_pool
     [num_slots,D] fp32; src_slot, dst_slot int32 [B] on the device (negative
     src = zero state, negative dst = not written). Returns out [B,K,D]."""
-    lib = load_library()
-    B, K, D = _dims(x, "x", 3)
-    code, dev = _dtype_code(x), x.device
-    _need(x, "x")
-    _need(alpha, "alpha", x.dtype, x.shape, dev)
-    _opt(beta, "beta", x.dtype, x.shape, dev)
-    num_slots, _ = _dims(state_pool, "state_pool", 2)
-    _need(state_pool, "state_pool", torch.float32, (num_slots, D), dev)
-    _need(src_slot, "src_slot", torch.int32, (B,), dev)
-    _need(dst_slot, "dst_slot", torch.int32, (B,), dev)
-    _opt(out, "out", x.dtype, x.shape, dev)
-    with _On(dev, stream) as st:
-        if out is None:
-            out = torch.empty_like(x)
-        rc = lib.gdn_scan_decode(x.data_ptr(), alpha.data_ptr(), _ptr(beta),
-                                 state_pool.data_ptr(), num_slots, src_slot.data_ptr(),
-                                 dst_slot.data_ptr(), out.data_ptr(), B, K, D, code, flags, st)
-    _check(rc)
+    lib = _lib or load_library()
+    code, index, shape = _start(x, "x", 3)
+    B, K, D = shape
+    _like(alpha, "alpha", x.dtype, shape, index)
+    if beta is not None:
+        _like(beta, "beta", x.dtype, shape, index)
+    if not isinstance(state_pool, torch.Tensor) or state_pool.dim() != 2:
+        raise ValueError("state_pool must be a tensor of shape [num_slots, D]")
+    num_slots = state_pool.shape[0]
+    _like(state_pool, "state_pool", torch.float32, (num_slots, D), index)
+    _like(src_slot, "src_slot", torch.int32, (B,), index)
+    _like(dst_slot, "dst_slot", torch.int32, (B,), index)
+    _on_gpu(index)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _like(out, "out", x.dtype, shape, index)
+    rc = lib.gdn_scan_decode(x.data_ptr(), alpha.data_ptr(), _ptr(beta), state_pool.data_ptr(),
+                             num_slots, src_slot.data_ptr(), dst_slot.data_ptr(), out.data_ptr(),
+                             B, K, D, code, flags, _raw_stream(index))
+    if rc:
+        _check(rc)
     return out
 
 
+def _rows(t, name):
+    """(type code, device index, rows, columns) of a tensor of rows."""
+    if t.dim() < 1 or t.shape[-1] < 1:
+        raise ValueError(f"{name} must have a last dimension of at least 1, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    D = t.shape[-1]
+    return _dtype_code(t), t.get_device(), t.numel() // D, D
+
+
+@_on_stream("x")
 def gdn_rms_norm(x, weight, residual=None, *, eps: float = 1e-6, group: int = 0,
                  want_out: bool = True, want_out8: bool = False, want_residual: bool = True,
-                 out=None, out8=None, scales=None, residual_out=None, stream=None):
+                 out=None, out8=None, scales=None, residual_out=None):
     """RMS norm over the last dimension of x (any leading dimensions), with the
     residual's addition and an output in 8 bits. x, residual, weight [D] of one
     dtype. Returns (out, out8, scales, residual_out), None where not wanted:
     out8 is torch.float8_e4m3fn with fp32 scales, one per row (group 0, shape
     [..., 1]) or per 128 columns (group 128, [..., ceil(D / 128)]);
     residual_out is x + residual (pass residual itself to update it in place)."""
-    lib = load_library()
-    code, dev = _dtype_code(x), x.device
-    if x.dim() < 1 or x.shape[-1] < 1:
-        raise ValueError(f"x must have a last dimension of at least 1, got {tuple(x.shape)}")
-    D = x.shape[-1]
-    rows = x.numel() // D
-    _need(x, "x")
-    _need(weight, "weight", x.dtype, (D,), dev)
-    _opt(residual, "residual", x.dtype, x.shape, dev)
+    lib = _lib or load_library()
+    code, index, rows, D = _rows(x, "x")
+    dt, shape = x.dtype, x.shape
+    _like(weight, "weight", dt, (D,), index)
+    if group != 0 and group != 128:
+        raise ValueError(f"group must be 0 (one scale per row) or 128, got {group}")
     if residual is None and residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    if group not in (0, 128):
-        raise ValueError(f"group must be 0 (one scale per row) or 128, got {group}")
-    _opt(out, "out", x.dtype, x.shape, dev)
-    _opt(out8, "out8", torch.float8_e4m3fn, x.shape, dev)
-    sshape = (*x.shape[:-1], 1 if group == 0 else -(-D // 128))
-    _opt(scales, "scales", torch.float32, sshape, dev)
-    _opt(residual_out, "residual_out", x.dtype, x.shape, dev)
-    want_out8 = want_out8 or out8 is not None or scales is not None
-    with _On(dev, stream) as st:
-        if out is None and want_out:
-            out = torch.empty_like(x)
-        if want_out8:
-            out8 = torch.empty_like(x, dtype=torch.float8_e4m3fn) if out8 is None else out8
-            if scales is None:
-                scales = torch.empty(sshape, dtype=torch.float32, device=dev)
-        if residual is not None and residual_out is None and want_residual:
+    _on_gpu(index)
+    if residual is not None:
+        _like(residual, "residual", dt, shape, index)
+        if residual_out is not None:
+            _like(residual_out, "residual_out", dt, shape, index)
+        elif want_residual:
             residual_out = torch.empty_like(x)
-        rc = lib.gdn_rms_norm(x.data_ptr(), _ptr(residual), weight.data_ptr(),
-                              _ptr(residual_out), _ptr(out), _ptr(out8), _ptr(scales), group,
-                              rows, D, code, eps, st)
-    _check(rc)
+    if out is not None:
+        _like(out, "out", dt, shape, index)
+    elif want_out:
+        out = torch.empty_like(x)
+    if want_out8 or out8 is not None or scales is not None:
+        sshape = (*shape[:-1], 1 if group == 0 else -(-D // 128))
+        if out8 is None:
+            out8 = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+        else:
+            _like(out8, "out8", torch.float8_e4m3fn, shape, index)
+        if scales is None:
+            scales = x.new_empty(sshape, dtype=torch.float32)
+        else:
+            _like(scales, "scales", torch.float32, sshape, index)
+    rc = lib.gdn_rms_norm(x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(residual_out),
+                          _ptr(out), _ptr(out8), _ptr(scales), group, rows, D, code, eps,
+                          _raw_stream(index))
+    if rc:
+        _check(rc)
     return out, out8, scales, residual_out
 
 
+@_on_stream("dout")
 def gdn_rms_norm_backward(dout, r, weight, dresidual=None, *, eps: float = 1e-6,
-                          want_dweight: bool = True, dx=None, dweight=None, workspace="auto",
-                          stream=None):
+                          want_dweight: bool = True, dx=None, dweight=None, workspace="auto"):
     """Gradients of gdn_rms_norm at the row sums r (residual_out, or x without
     a residual): dout, r [..., D]; dresidual, the gradient that arrives at
     residual_out, or None. Returns (dx, dweight fp32 [D] or None); dx is the
     gradient of x and of residual alike and may be dresidual itself."""
-    lib = load_library()
-    code, dev = _dtype_code(r), r.device
-    if r.dim() < 1 or r.shape[-1] < 1:
-        raise ValueError(f"r must have a last dimension of at least 1, got {tuple(r.shape)}")
-    D = r.shape[-1]
-    rows = r.numel() // D
-    _need(r, "r")
-    _need(dout, "dout", r.dtype, r.shape, dev)
-    _need(weight, "weight", r.dtype, (D,), dev)
-    _opt(dresidual, "dresidual", r.dtype, r.shape, dev)
-    _opt(dx, "dx", r.dtype, r.shape, dev)
-    _opt(dweight, "dweight", torch.float32, (D,), dev)
-    on = _On(dev, stream)
-    with on as st:
-        if dx is None:
-            dx = torch.empty_like(r)
-        if dweight is None and want_dweight:
-            dweight = torch.empty(D, dtype=torch.float32, device=dev)
-        wp, wb, _keep = None, 0, None
-        if dweight is not None:
-            wp, wb, _keep = _scratch(workspace, lambda: lib.gdn_rms_norm_workspace_size(rows, D),
-                                     dev, on.stream)
-        rc = lib.gdn_rms_norm_backward(dout.data_ptr(), r.data_ptr(), weight.data_ptr(),
-                                       _ptr(dresidual), dx.data_ptr(), _ptr(dweight), rows, D,
-                                       code, eps, wp, wb, st)
-    _check(rc)
+    lib = _lib or load_library()
+    code, index, rows, D = _rows(dout, "dout")
+    dt, shape = dout.dtype, dout.shape
+    _like(r, "r", dt, shape, index)
+    _like(weight, "weight", dt, (D,), index)
+    if dresidual is not None:
+        _like(dresidual, "dresidual", dt, shape, index)
+    _on_gpu(index)
+    if dx is None:
+        dx = torch.empty_like(r)
+    else:
+        _like(dx, "dx", dt, shape, index)
+    if dweight is not None:
+        _like(dweight, "dweight", torch.float32, (D,), index)
+    elif want_dweight:
+        dweight = torch.empty_like(weight, dtype=torch.float32)
+    wp, wb, _keep = None, 0, None
+    if dweight is not None:
+        wp, wb, _keep = _scratch(workspace, lambda: lib.gdn_rms_norm_workspace_size(rows, D),
+                                 index, dweight)
+    rc = lib.gdn_rms_norm_backward(dout.data_ptr(), r.data_ptr(), weight.data_ptr(),
+                                   _ptr(dresidual), dx.data_ptr(), _ptr(dweight), rows, D, code,
+                                   eps, wp, wb, _raw_stream(index))
+    if rc:
+        _check(rc)
     return dx, dweight
 
 
+@_on_stream("logits")
 def gdn_beam_select(logits, scores, *, finished=None, eos: int = -1, beam_slots=None,
                     new_scores=None, tokens=None, parents=None, new_finished=None,
-                    src_slots=None, workspace="auto", stream=None):
+                    src_slots=None, workspace="auto"):
     """Beam search's selection. logits [B,W,V] (bf16 or fp32); scores [B,W]
     fp32, the beams' summed log-probabilities; finished uint8 [B,W] or None;
     eos the end token (-1: none); beam_slots int32 [B,W] or None, the beams'
@@ -695,64 +739,72 @@ def gdn_beam_select(logits, scores, *, finished=None, eos: int = -1, beam_slots=
     src_slots the parents' slots (the src_slot of the next decode call, or
     gdn_gather_states' index). new_finished is None without eos, src_slots
     without beam_slots."""
-    lib = load_library()
-    B, W, V = _dims(logits, "logits", 3)
-    code, dev = _dtype_code(logits), logits.device
-    _need(logits, "logits")
+    lib = _lib or load_library()
+    code, index, (B, W, V) = _start(logits, "logits", 3)
     shape = (B, W)
-    _need(scores, "scores", torch.float32, shape, dev)
-    _opt(finished, "finished", torch.uint8, shape, dev)
-    _opt(beam_slots, "beam_slots", torch.int32, shape, dev)
-    for t, name, dtype in ((new_scores, "new_scores", torch.float32),
-                           (tokens, "tokens", torch.int32), (parents, "parents", torch.int32),
-                           (new_finished, "new_finished", torch.uint8),
-                           (src_slots, "src_slots", torch.int32)):
-        if t is not None:
-            _need(t, name, dtype, shape, dev)
-    if finished is not None and eos < 0:
-        raise ValueError("finished needs eos")
-    on = _On(dev, stream)
-    with on as st:
-        if new_scores is None:
-            new_scores = torch.empty(shape, dtype=torch.float32, device=dev)
-        if tokens is None:
-            tokens = torch.empty(shape, dtype=torch.int32, device=dev)
-        if parents is None:
-            parents = torch.empty(shape, dtype=torch.int32, device=dev)
-        if new_finished is None and eos >= 0:
-            new_finished = torch.empty(shape, dtype=torch.uint8, device=dev)
-        if src_slots is None and beam_slots is not None:
-            src_slots = torch.empty(shape, dtype=torch.int32, device=dev)
-        wp, wb, _keep = _scratch(workspace, lambda: lib.gdn_beam_workspace_size(B, W, V, code),
-                                 dev, on.stream)
-        rc = lib.gdn_beam_select(logits.data_ptr(), scores.data_ptr(), _ptr(finished),
-                                 _ptr(beam_slots), new_scores.data_ptr(), tokens.data_ptr(),
-                                 parents.data_ptr(), _ptr(new_finished), _ptr(src_slots), B, W, V,
-                                 eos, code, wp, wb, st)
-    _check(rc)
+    _like(scores, "scores", torch.float32, shape, index)
+    if finished is not None:
+        _like(finished, "finished", torch.uint8, shape, index)
+        if eos < 0:
+            raise ValueError("finished needs eos")
+    if beam_slots is not None:
+        _like(beam_slots, "beam_slots", torch.int32, shape, index)
+    _on_gpu(index)
+    if new_scores is None:
+        new_scores = torch.empty_like(scores)
+    else:
+        _like(new_scores, "new_scores", torch.float32, shape, index)
+    if tokens is None:
+        tokens = torch.empty_like(scores, dtype=torch.int32)
+    else:
+        _like(tokens, "tokens", torch.int32, shape, index)
+    if parents is None:
+        parents = torch.empty_like(tokens)
+    else:
+        _like(parents, "parents", torch.int32, shape, index)
+    if new_finished is not None:
+        _like(new_finished, "new_finished", torch.uint8, shape, index)
+    elif eos >= 0:
+        new_finished = torch.empty_like(scores, dtype=torch.uint8)
+    if src_slots is not None:
+        _like(src_slots, "src_slots", torch.int32, shape, index)
+    elif beam_slots is not None:
+        src_slots = torch.empty_like(beam_slots)
+    wp, wb, _keep = _scratch(workspace, lambda: lib.gdn_beam_workspace_size(B, W, V, code), index,
+                             scores)
+    rc = lib.gdn_beam_select(logits.data_ptr(), scores.data_ptr(), _ptr(finished),
+                             _ptr(beam_slots), new_scores.data_ptr(), tokens.data_ptr(),
+                             parents.data_ptr(), _ptr(new_finished), _ptr(src_slots), B, W, V,
+                             eos, code, wp, wb, _raw_stream(index))
+    if rc:
+        _check(rc)
     return new_scores, tokens, parents, new_finished, src_slots
 
 
-def gdn_gather_states(states, index, *, out=None, stream=None):
+@_on_stream("states")
+def gdn_gather_states(states, index, *, out=None):
     """Rows of a state buffer in a new order: out[i] = states[index[i]], any
     dtype, rows of a multiple of 16 bytes. index int32 [R] on the device (negative:
     zeros; past the end: bytes of 0xff). out must not overlap states."""
-    lib = load_library()
-    if not isinstance(states, torch.Tensor) or states.dim() < 1:
-        raise ValueError("states must be a tensor with a first dimension of rows")
-    dev = states.device
-    _need(states, "states")
-    R = _dims(index, "index", 1)[0]
-    _need(index, "index", torch.int32, device=dev)
+    lib = _lib or load_library()
+    dev = states.get_device()
+    if states.dim() < 1 or not states.is_contiguous():
+        raise ValueError("states must be contiguous, with a first dimension of rows")
+    if not isinstance(index, torch.Tensor) or index.dim() != 1:
+        raise ValueError("index must be a one-dimensional tensor")
+    _like(index, "index", torch.int32, index.shape, dev)
+    R = index.shape[0]
     shape = (R, *states.shape[1:])
-    row_bytes = math.prod(states.shape[1:]) * states.element_size()
-    _opt(out, "out", states.dtype, shape, dev)
-    with _On(dev, stream) as st:
-        if out is None:
-            out = torch.empty(shape, dtype=states.dtype, device=dev)
-        rc = lib.gdn_gather_states(states.data_ptr(), states.shape[0], index.data_ptr(),
-                                   out.data_ptr(), R, row_bytes, st)
-    _check(rc)
+    row_bytes = math.prod(shape[1:]) * states.element_size()
+    _on_gpu(dev)
+    if out is None:
+        out = states.new_empty(shape)
+    else:
+        _like(out, "out", states.dtype, shape, dev)
+    rc = lib.gdn_gather_states(states.data_ptr(), states.shape[0], index.data_ptr(),
+                               out.data_ptr(), R, row_bytes, _raw_stream(dev))
+    if rc:
+        _check(rc)
     return out
 
 
