@@ -19,8 +19,15 @@ namespace gdn {
 
 namespace {
 
-constexpr float kE4m3Max = 448.f;
+constexpr float kE4m3Inv = 1.f / 448.f;  // of the largest e4m3 value
 constexpr float kScaleFloor = 0x1p-100f;  // groups of zeros keep a finite scale and its inverse
+
+// 1 / sqrt(x) to about a unit in its last place: the instruction's value and one
+// Newton step (x > 0: a mean of squares and eps).
+__device__ __forceinline__ float inv_sqrt(float x) {
+    const float s = __builtin_amdgcn_rsqf(x);
+    return s * fmaf(-0.5f * x * s, s, 1.5f);
+}
 
 __device__ __forceinline__ float row16_max(float x) {
     x = fmaxf(x, GDN_DPP(x, 0xB1));
@@ -122,39 +129,48 @@ template <int TPR> __device__ __forceinline__ int row_threads() {
     return TPR == 0 ? (int)blockDim.x : TPR;
 }
 
-template <typename DT, bool VEC, int TPR, int CH>
-__global__ __launch_bounds__(1024) void norm_kernel(NormParams p) {
-    __shared__ float s_red[2][16];
-    const int tpr = row_threads<TPR>();
-    const int j = TPR == 0 ? threadIdx.x : threadIdx.x % tpr;
-    const int64_t row = TPR == 0 ? blockIdx.x
-                                 : (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
-    const int D = p.D;
-    const bool live = row < p.rows;  // no early exit: the lanes of a wave reduce together
-    const int64_t at = row * D;
+// One row of a thread: x and the residual as fp32, from memory.
+template <typename DT, bool VEC, int TPR, int CH> struct NormRow {
     float r[CH][8];
+
+    __device__ __forceinline__ void load(const NormParams &p, int64_t row, bool live, int tpr,
+                                         int j) {
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            const int c = (k * tpr + j) * 8, left = live ? p.D - c : 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r[k][e] = 0.f;
+            if (left <= 0) continue;
+            load8<DT, VEC>(reinterpret_cast<const DT *>(p.x) + row * p.D + c, left, r[k]);
+            if (p.res) {
+                float q[8];
+                load8<DT, VEC>(reinterpret_cast<const DT *>(p.res) + row * p.D + c, left, q);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) r[k][e] += q[e];
+            }
+        }
+    }
+};
+
+// Everything behind a row's loads. A row past the last one takes part with
+// zeros, for the lanes of a wave reduce together.
+template <typename DT, bool VEC, int TPR, int CH>
+__device__ __forceinline__ void norm_row(const NormParams &p, int64_t row, int tpr, int j,
+                                         float (&r)[CH][8], float (*s_red)[16]) {
+    const int D = p.D;
+    const bool live = row < p.rows;
+    const int64_t at = row * D;
     float ss = 0.f;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
         const int c = (k * tpr + j) * 8, left = live ? D - c : 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) r[k][e] = 0.f;
-        if (left > 0) {
-            load8<DT, VEC>(reinterpret_cast<const DT *>(p.x) + at + c, left, r[k]);
-            if (p.res) {
-                float q[8];
-                load8<DT, VEC>(reinterpret_cast<const DT *>(p.res) + at + c, left, q);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) r[k][e] += q[e];
-                if (p.res_out)
-                    store8<DT, VEC>(reinterpret_cast<DT *>(p.res_out) + at + c, left, r[k]);
-            }
-        }
+        if (left > 0 && p.res_out)
+            store8<DT, VEC>(reinterpret_cast<DT *>(p.res_out) + at + c, left, r[k]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss = fmaf(r[k][e], r[k][e], ss);
     }
     ss = row_reduce<TPR, SumOp>(ss, s_red[0]);
-    const float s = 1.f / sqrtf(ss / (float)D + p.eps);
+    const float s = inv_sqrt(fmaf(ss, p.inv_d, p.eps));
     float most = 0.f;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
@@ -173,8 +189,8 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p) {
         if (p.group == 0) {
             most = fmaxf(most, m);
         } else {  // 128 columns: the 16 lanes of a DPP row
-            m = fmaxf(row16_max(m) / kE4m3Max, kScaleFloor);
-            const float inv = 1.f / m;
+            m = fmaxf(row16_max(m) * kE4m3Inv, kScaleFloor);
+            const float inv = __builtin_amdgcn_rcpf(m);
 #pragma unroll
             for (int e = 0; e < 8; ++e) r[k][e] *= inv;
             if (left > 0) {
@@ -185,7 +201,8 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p) {
     }
     if (p.out8 && p.group == 0) {
         most = row_reduce<TPR, MaxOp>(most, s_red[1]);
-        const float scale = fmaxf(most / kE4m3Max, kScaleFloor), inv = 1.f / scale;
+        const float scale = fmaxf(most * kE4m3Inv, kScaleFloor);
+        const float inv = __builtin_amdgcn_rcpf(scale);
         if (live && j == 0) p.scales[row] = scale;
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
@@ -195,6 +212,23 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p) {
             if (left > 0) store8_e4m3<VEC>(p.out8 + at + c, left, r[k]);
         }
     }
+}
+
+// NROWS rows per thread, their loads issued together.
+template <typename DT, bool VEC, int TPR, int CH, int NROWS>
+__global__ __launch_bounds__(1024) void norm_kernel(NormParams p) {
+    __shared__ float s_red[2][16];
+    const int tpr = row_threads<TPR>();
+    const int j = TPR == 0 ? threadIdx.x : threadIdx.x % tpr;
+    const int per = TPR == 0 ? 1 : blockDim.x / tpr;
+    const int64_t row0 = (int64_t)blockIdx.x * per * NROWS + (TPR == 0 ? 0 : threadIdx.x / tpr);
+    NormRow<DT, VEC, TPR, CH> rows[NROWS];
+#pragma unroll
+    for (int i = 0; i < NROWS; ++i)
+        rows[i].load(p, row0 + i * per, row0 + i * per < p.rows, tpr, j);
+#pragma unroll
+    for (int i = 0; i < NROWS; ++i)
+        norm_row<DT, VEC, TPR, CH>(p, row0 + i * per, tpr, j, rows[i].r, s_red);
 }
 
 // dx per row, and each workgroup's share of dw: a thread keeps the sums of its
@@ -265,8 +299,8 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormBackwardParams 
             ss = row_reduce<TPR, SumOp>(ss, s_red[0]);
             dot = row_reduce<TPR, SumOp>(dot, s_red[1]);
         }
-        const float s = 1.f / sqrtf(ss / (float)D + p.eps);
-        const float m = s * s * s * (dot / (float)D);
+        const float s = inv_sqrt(fmaf(ss, p.inv_d, p.eps));
+        const float m = s * s * s * (dot * p.inv_d);
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
             const int c = (k * tpr + j) * 8, left = live ? D - c : 0;
@@ -313,20 +347,46 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormBackwardParams 
     }
 }
 
-// dw[c] = sum over the partials, 16 threads per column and a fixed order.
+// dw[c] = sum over the partials in a fixed order: 32 columns per workgroup, 4
+// per lane where a partial row starts on 16 bytes, 128 threads (or 32) beside
+// each other down the partials.
+template <int VEC>
 __global__ __launch_bounds__(1024) void norm_dweight_kernel(const float *partial, int count,
                                                             float *dw, int D) {
-    __shared__ float s_sum[16][64];
-    const int lane = threadIdx.x & 63, part = threadIdx.x >> 6;
-    const int c = blockIdx.x * 64 + lane;
-    float sum = 0.f;
+    constexpr int kLanes = 32 / VEC, kParts = 1024 / kLanes;
+    __shared__ float s_sum[16][32];
+    const int l = threadIdx.x % kLanes, part = threadIdx.x / kLanes;
+    const int c = blockIdx.x * 32 + l * VEC;
+    float sum[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) sum[e] = 0.f;
     if (c < D)
-        for (int i = part; i < count; i += 16) sum += partial[(int64_t)i * D + c];
-    s_sum[part][lane] = sum;
+#pragma unroll 4
+        for (int i = part; i < count; i += kParts) {
+            const float *from = partial + (int64_t)i * D + c;
+            if constexpr (VEC == 4) {
+                const f32x4 x = *reinterpret_cast<const f32x4 *>(from);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[e] += x[e];
+            } else {
+                sum[0] += from[0];
+            }
+        }
+    // the parts of a wave, then the 16 waves
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+#pragma unroll
+        for (int o = kLanes; o < 64; o <<= 1) sum[e] += __shfl_xor(sum[e], o);
+    if ((threadIdx.x & 63) < kLanes)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) s_sum[threadIdx.x >> 6][l * VEC + e] = sum[e];
     __syncthreads();
-    if (part == 0 && c < D) {
-        for (int i = 1; i < 16; ++i) sum += s_sum[i][lane];
-        dw[c] = sum;
+    const int o = blockIdx.x * 32 + threadIdx.x;
+    if (threadIdx.x < 32 && o < D) {
+        float all = s_sum[0][threadIdx.x];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) all += s_sum[i][threadIdx.x];
+        dw[o] = all;
     }
 }
 
@@ -367,7 +427,15 @@ struct RunNorm {
     const NormParams &p;
     hipStream_t stream;
     template <typename DT, bool VEC, int TPR, int CH> hipError_t run(const NormPlan &n) const {
-        hipLaunchKernelGGL((norm_kernel<DT, VEC, TPR, CH>),
+        if constexpr (TPR != 0) {
+            if (p.rows >= (int64_t)n.per * 2 * 4096) {
+                hipLaunchKernelGGL((norm_kernel<DT, VEC, TPR, CH, 2>),
+                                   dim3((unsigned)((p.rows + 2 * n.per - 1) / (2 * n.per))),
+                                   dim3(n.threads), 0, stream, p);
+                return hipGetLastError();
+            }
+        }
+        hipLaunchKernelGGL((norm_kernel<DT, VEC, TPR, CH, 1>),
                            dim3((unsigned)((p.rows + n.per - 1) / n.per)), dim3(n.threads), 0,
                            stream, p);
         return hipGetLastError();
@@ -404,9 +472,15 @@ hipError_t launch_norm_backward(const NormBackwardParams &p, int dtype, hipStrea
             with_norm_types(dtype, p.D, plan_norm(p.D), RunNormBackward{p, stream});
         if (e != hipSuccess) return e;
     }
-    if (p.dw)
-        hipLaunchKernelGGL(norm_dweight_kernel, dim3((unsigned)((p.D + 63) / 64)), dim3(1024), 0,
-                           stream, p.partial, count, p.dw, p.D);
+    if (p.dw) {
+        const dim3 grid((unsigned)((p.D + 31) / 32)), block(1024);
+        if (p.D % 4 == 0)
+            hipLaunchKernelGGL(norm_dweight_kernel<4>, grid, block, 0, stream, p.partial, count,
+                               p.dw, p.D);
+        else
+            hipLaunchKernelGGL(norm_dweight_kernel<1>, grid, block, 0, stream, p.partial, count,
+                               p.dw, p.D);
+    }
     return hipGetLastError();
 }
 

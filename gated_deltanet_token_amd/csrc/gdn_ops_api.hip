@@ -181,7 +181,7 @@ gdn_status_t gdn_rms_norm(const void *x, const void *residual, const void *weigh
                                        group, rows, D, dtype, eps);
     if (st != GDN_OK || rows == 0) return st;
     gdn::NormParams p{x, residual, weight, residual_out, out, static_cast<uint8_t *>(out8),
-                      scales, group, rows, D, eps};
+                      scales, group, rows, D, eps, 1.f / (float)D};
     const hipError_t e = gdn::launch_norm(p, code(dtype), stream);
     return e == hipSuccess ? GDN_OK : gdn::hip_fail(e, "gdn_rms_norm launch");
 }
@@ -201,7 +201,7 @@ gdn_status_t gdn_rms_norm_backward(const void *dout, const void *r, const void *
                             workspace, workspace_bytes, gdn_rms_norm_workspace_size(rows, D));
     if (st != GDN_OK || (rows == 0 && !dweight)) return st;
     gdn::NormBackwardParams p{dout, r, weight, dresidual, dx, dweight,
-                              static_cast<float *>(workspace), rows, D, eps};
+                              static_cast<float *>(workspace), rows, D, eps, 1.f / (float)D};
     const hipError_t e = gdn::launch_norm_backward(p, code(dtype), stream);
     return e == hipSuccess ? GDN_OK : gdn::hip_fail(e, "gdn_rms_norm_backward launch");
 }

@@ -62,7 +62,7 @@ struct NormParams {
     int32_t group;
     int64_t rows;
     int32_t D;
-    float eps;
+    float eps, inv_d;  // inv_d: 1 / D
 };
 
 struct NormBackwardParams {
@@ -72,7 +72,7 @@ struct NormBackwardParams {
     float *partial;  // [norm_partials(rows, D)][D]
     int64_t rows;
     int32_t D;
-    float eps;
+    float eps, inv_d;  // inv_d: 1 / D
 };
 
 hipError_t launch_norm(const NormParams &p, int dtype, hipStream_t stream);

@@ -377,12 +377,12 @@ hipError_t with_scan_gates(bool tied, bool logits, F &&f) {
         return logits ? f.template run<DT, VEC, true, true>() : f.template run<DT, VEC, true, false>();
     return logits ? f.template run<DT, VEC, false, true>() : f.template run<DT, VEC, false, false>();
 }
-template <typename F>
+template <int BVEC, typename F>
 hipError_t with_scan_types(int dtype, int32_t D, const void *b, uint32_t flags, F &&f) {
     const bool tied = b == nullptr, logits = flags & GDN_GATE_LOGITS;
     if (dtype == 1)
-        return D % 8 == 0 ? with_scan_gates<__bf16, 8>(tied, logits, f)
-                          : with_scan_gates<__bf16, 1>(tied, logits, f);
+        return D % BVEC == 0 ? with_scan_gates<__bf16, BVEC>(tied, logits, f)
+                             : with_scan_gates<__bf16, 1>(tied, logits, f);
     return D % 4 == 0 ? with_scan_gates<float, 4>(tied, logits, f)
                       : with_scan_gates<float, 1>(tied, logits, f);
 }
@@ -425,7 +425,11 @@ bool scan_wants_split(int64_t nseq, int64_t tokens, int64_t ncb, bool packed, in
     return tokens > GDN_SCAN_TILE && nseq * ncb < 8 * (int64_t)cus;
 }
 
-int scan_cols(int32_t D, int dtype) {
+constexpr int kBackVec = 4;  // columns per thread of the bf16 backward kernel
+
+int scan_cols(int32_t D, int dtype, bool back) {
+    if (dtype == 1 && back)
+        return D % kBackVec == 0 ? ScanShape<__bf16, kBackVec>::kCols : ScanShape<__bf16, 1>::kCols;
     if (dtype == 1) return D % 8 == 0 ? ScanShape<__bf16, 8>::kCols : ScanShape<__bf16, 1>::kCols;
     return D % 4 == 0 ? ScanShape<float, 4>::kCols : ScanShape<float, 1>::kCols;
 }
@@ -433,11 +437,11 @@ int scan_cols(int32_t D, int dtype) {
 // Fills sp and clears the workspace when the call is to be cut; sp.slots is 0
 // when not.
 hipError_t prepare_split(const ScanParams &p, int dtype, int cus, void *ws, size_t ws_bytes,
-                         ScanSplit &sp, hipStream_t stream) {
+                         bool back, ScanSplit &sp, hipStream_t stream) {
     sp = ScanSplit{};
     const bool packed = p.cu != nullptr;
     const int64_t tokens = packed ? p.total : p.T;
-    const int cols = scan_cols(p.D, dtype);
+    const int cols = scan_cols(p.D, dtype, back);
     const ScanLayout l = scan_layout(p.N, tokens, p.D, cols, packed);
     if (!ws || ws_bytes < (size_t)l.bytes ||
         !scan_wants_split(p.N, tokens, l.width / cols, packed, cus))
@@ -506,30 +510,34 @@ struct RunDecode {
 
 size_t scan_workspace_bytes(int64_t nseq, int64_t tokens, int32_t D, int dtype, bool packed,
                             int cus) {
-    const int cols = scan_cols(D, dtype);
-    const ScanLayout l = scan_layout(nseq, tokens, D, cols, packed);
-    if (!scan_wants_split(nseq, tokens, l.width / cols, packed, cus)) return 0;
-    return (size_t)((l.bytes + 15) / 16 * 16);
+    int64_t most = 0;  // of the forward and the backward call
+    for (const bool back : {false, true}) {
+        const int cols = scan_cols(D, dtype, back);
+        const ScanLayout l = scan_layout(nseq, tokens, D, cols, packed);
+        if (scan_wants_split(nseq, tokens, l.width / cols, packed, cus) && l.bytes > most)
+            most = l.bytes;
+    }
+    return (size_t)most;
 }
 
 hipError_t launch_scan(const ScanParams &p, int dtype, int cus, void *ws, size_t ws_bytes,
                        hipStream_t stream) {
     ScanSplit sp;
-    const hipError_t e = prepare_split(p, dtype, cus, ws, ws_bytes, sp, stream);
+    const hipError_t e = prepare_split(p, dtype, cus, ws, ws_bytes, false, sp, stream);
     if (e != hipSuccess) return e;
-    return with_scan_types(dtype, p.D, p.b, p.flags, RunForward{p, sp, stream});
+    return with_scan_types<8>(dtype, p.D, p.b, p.flags, RunForward{p, sp, stream});
 }
 
 hipError_t launch_scan_backward(const ScanParams &p, int dtype, int cus, void *ws,
                                 size_t ws_bytes, hipStream_t stream) {
     ScanSplit sp;
-    const hipError_t e = prepare_split(p, dtype, cus, ws, ws_bytes, sp, stream);
+    const hipError_t e = prepare_split(p, dtype, cus, ws, ws_bytes, true, sp, stream);
     if (e != hipSuccess) return e;
-    return with_scan_types(dtype, p.D, p.b, p.flags, RunBackward{p, sp, stream});
+    return with_scan_types<kBackVec>(dtype, p.D, p.b, p.flags, RunBackward{p, sp, stream});
 }
 
 hipError_t launch_scan_decode(const ScanDecodeParams &p, int dtype, hipStream_t stream) {
-    return with_scan_types(dtype, p.D, p.b, p.flags, RunDecode{p, stream});
+    return with_scan_types<8>(dtype, p.D, p.b, p.flags, RunDecode{p, stream});
 }
 
 }  // namespace gdn
