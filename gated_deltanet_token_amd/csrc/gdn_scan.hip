@@ -32,7 +32,7 @@ __device__ __forceinline__ ScanTile take_tile(const ScanParams &p, const ScanSpl
         *s_ticket = (int)__hip_atomic_fetch_add(sp.ticket + chain, 1u, __ATOMIC_RELAXED,
                                                 __HIP_MEMORY_SCOPE_AGENT);
     __syncthreads();
-    int64_t k = *s_ticket;
+    int64_t k = __builtin_amdgcn_readfirstlane(*s_ticket);  // uniform, and known to be
     ScanTile t;
     if (p.cu) {
         if (BACK) k = sp.slots - 1 - k;
@@ -83,7 +83,8 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_forward_k
     }
     const int64_t prow = p.prefix_out ? scan_prefix_row(p, n, base) : 0;
 
-    for (int64_t t0 = mine.tile * Sh::kRows; t0 < len; t0 += Sh::kRows) {
+    int64_t t0 = mine.tile * Sh::kRows;
+    do {
         const int left = (int)(len - t0 < Sh::kRows ? len - t0 : Sh::kRows);  // tokens here
         const int64_t tile = (base + t0) * D;
         const DT *xt = as<DT>(p.x, tile), *at = as<DT>(p.a, tile);
@@ -147,34 +148,30 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_forward_k
         }
         __syncthreads();
         // a thread reads and rewrites its own places only: no third barrier
-        Raw<float, VEC> h;
+        float h[VEC];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) h.v[e] = s_h[g][l * VEC + e];
+        for (int e = 0; e < VEC; ++e) h[e] = s_h[g][l * VEC + e];
         DT *ot = as<DT>(p.out, tile);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            Raw<DT, VEC> o;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                h.v[e] = fmaf(al[r][e], h[e], u[r][e]);
-                o.set(e, h[e]);
-            }
+            for (int e = 0; e < VEC; ++e) h[e] = fmaf(al[r][e], h[e], u[r][e]);
             if (on && g * R + r < left)
-                store_raw(ot, ((uint32_t)(g * R + r) * D + c0) * sizeof(DT), o);
+                store_raw(ot, ((uint32_t)(g * R + r) * D + c0) * sizeof(DT), pack<DT>(h));
         }
         // past the end h stays the last token's state
         if (on && p.prefix_out && ((g + 1) * R & 63) == 0 && (g + 1) * R <= left) {
             const int64_t blk = scan_block_ending(p, t0 + (g + 1) * R);
-            if (blk >= 0) store_raw(p.prefix_out + (prow + blk) * D, c0 * 4, h);
+            if (blk >= 0) store_raw(p.prefix_out + (prow + blk) * D, c0 * 4, pack<float>(h));
         }
         if (on && p.hT && t0 + left == len && g == (left - 1) / R)
-            store_raw(p.hT + (int64_t)n * D, c0 * 4, h);
-        if constexpr (SPLIT) return;
-    }
+            store_raw(p.hT + (int64_t)n * D, c0 * 4, pack<float>(h));
+        t0 += Sh::kRows;
+    } while (!SPLIT && t0 < len);
 }
 
 template <typename DT, int VEC, bool TIED, bool LOGITS, bool SPLIT>
-__global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_backward_kernel(
+__global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads), 4) void scan_backward_kernel(
     ScanParams p, int ncb, ScanSplit sp) {
     using Sh = ScanShape<DT, VEC>;
     constexpr int G = Sh::kGroups, C = Sh::kCols, R = Sh::kPer;
@@ -204,7 +201,8 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_backward_
     }
     const int64_t prow = p.prefix_in ? scan_prefix_row(p, n, base) : 0;
 
-    for (int64_t t0 = mine.tile * Sh::kRows; t0 >= 0; t0 -= Sh::kRows) {
+    int64_t t0 = mine.tile * Sh::kRows;
+    do {
         const int left = (int)(len - t0 < Sh::kRows ? len - t0 : Sh::kRows);
         const int64_t tile = (base + t0) * D;
         const DT *xt = as<DT>(p.x, tile), *at = as<DT>(p.a, tile), *yt = as<DT>(p.dout, tile);
@@ -242,6 +240,7 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_backward_
             s_a[g][l * VEC + e] = A;
             s_h[g][l * VEC + e] = H;
             s_k[g][l * VEC + e] = K;
+            __builtin_amdgcn_sched_barrier(0);  // one column's gates in registers at a time
         }
         __syncthreads();
         if (tid < C) {
@@ -278,47 +277,48 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_backward_
             carry = fmaf(A, carry, K);
         }
         __syncthreads();
-        forget_all(a);
-        if constexpr (!TIED) forget_all(b);
-        Raw<float, VEC> before[R];
+        forget(x);
+        forget(a);
+        if constexpr (!TIED) forget(b);
+        forget(dy);
+        float ox[R][2], oa[R][2], ob[R][2];  // gradients of a pair of columns
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            float h = s_h[g][l * VEC + e];
+            float alpha[R], keep[R], beta[R], rest[R], before[R];
+            float h = s_h[g][l * VEC + e], c = s_k[g][l * VEC + e];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                float alpha, keep, beta;
-                before[r].v[e] = h;
-                gates<DT, TIED, LOGITS>(a[r][e], b[r][e], alpha, keep, beta);
-                h = fmaf(alpha, h, beta * x[r][e]);
+                before[r] = h;
+                gates<DT, TIED, LOGITS>(a[r][e], b[r][e], alpha[r], keep[r], beta[r]);
+                if constexpr (!TIED && LOGITS) write_pair(b[r][e], beta[r], rest[r], DT());
+                h = fmaf(alpha[r], h, beta[r] * x[r][e]);
             }
-        }
-        if constexpr (R > 4) {  // more rows than registers for their gates
-            forget_all(a);
-            if constexpr (!TIED) forget_all(b);
-        }
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            float c = s_k[g][l * VEC + e];
 #pragma unroll
             for (int r = R - 1; r >= 0; --r) {
                 const bool in = g * R + r < left;  // past the end c passes through
-                float alpha, keep, beta, rest = 0.f;
-                gates<DT, TIED, LOGITS>(a[r][e], b[r][e], alpha, keep, beta);
-                if constexpr (!TIED && LOGITS) sigmoid_pair<DT>(-b[r][e], beta, rest);
                 const float gr = (in ? dy[r][e] : 0.f) + c;
-                c = (in ? alpha : 1.f) * gr;
+                c = (in ? alpha[r] : 1.f) * gr;
                 // alpha' = -alpha (1 - alpha), beta' = beta (1 - beta) of the logits
                 const float xe = x[r][e];
-                float da = gr * (TIED ? before[r][e] - xe : before[r][e]);
-                if constexpr (LOGITS) da *= -alpha * keep;
+                float da = gr * (TIED ? before[r] - xe : before[r]);
+                if constexpr (LOGITS) da *= -alpha[r] * keep[r];
                 if constexpr (!TIED) {
                     float db = gr * xe;
-                    if constexpr (LOGITS) db *= beta * rest;
-                    b[r].set(e, db);
+                    if constexpr (LOGITS) db *= beta[r] * rest[r];
+                    ob[r][e & 1] = db;
                 }
-                a[r].set(e, da);
-                x[r].set(e, gr * beta);
+                oa[r][e & 1] = da;
+                ox[r][e & 1] = gr * beta[r];
             }
+            if ((e & 1) || VEC == 1) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    x[r].set(e & ~1, ox[r][0], ox[r][VEC > 1]);
+                    a[r].set(e & ~1, oa[r][0], oa[r][VEC > 1]);
+                    if constexpr (!TIED) b[r].set(e & ~1, ob[r][0], ob[r][VEC > 1]);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
         DT *dxt = as<DT>(p.dx, tile), *dat = as<DT>(p.da, tile), *dbt = as<DT>(p.db, TIED ? 0 : tile);
 #pragma unroll
@@ -329,10 +329,9 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_backward_
             store_raw(dat, i, a[r]);
             if constexpr (!TIED) store_raw(dbt, i, b[r]);
         }
-        if constexpr (SPLIT) {
-            if (mine.tile > 0) return;
-        }
-    }
+        t0 -= Sh::kRows;
+    } while (!SPLIT && t0 >= 0);
+    if (SPLIT && mine.tile > 0) return;
     if (chain && p.dh0) p.dh0[(int64_t)n * D + ch] = carry;
 }
 
@@ -347,26 +346,28 @@ __global__ __launch_bounds__(256) void scan_decode_kernel(ScanDecodeParams p) {
     const int c0 = (int)(i - b * per) * VEC;
     const int src = p.src[b], dst = p.dst[b];
     const bool bad = src >= p.num_slots || dst >= p.num_slots;
-    Raw<float, VEC> h;
+    float h[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) h.v[e] = bad ? __builtin_nanf("") : 0.f;
-    if (!bad && src >= 0) h = load_raw<VEC>(p.pool + (int64_t)src * p.D, c0 * 4);
+    for (int e = 0; e < VEC; ++e) h[e] = bad ? __builtin_nanf("") : 0.f;
+    if (!bad && src >= 0) {
+        const auto s = load_raw<VEC>(p.pool + (int64_t)src * p.D, c0 * 4);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) h[e] = s[e];
+    }
     for (int k = 0; k < p.K; ++k) {
         const int64_t at = (b * p.K + k) * p.D;
         const uint32_t i = c0 * sizeof(DT);
         const auto x = load_raw<VEC>(as<DT>(p.x, at), i), a = load_raw<VEC>(as<DT>(p.a, at), i);
         const auto w = TIED ? a : load_raw<VEC>(as<DT>(p.b, at), i);
-        Raw<DT, VEC> o;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             float alpha, keep, beta;
             gates<DT, TIED, LOGITS>(a[e], w[e], alpha, keep, beta);
-            h.v[e] = fmaf(alpha, h[e], beta * x[e]);
-            o.set(e, h[e]);
+            h[e] = fmaf(alpha, h[e], beta * x[e]);
         }
-        store_raw(as<DT>(p.out, at), i, o);
+        store_raw(as<DT>(p.out, at), i, pack<DT>(h));
     }
-    if (!bad && dst >= 0) store_raw(p.pool + (int64_t)dst * p.D, c0 * 4, h);
+    if (!bad && dst >= 0) store_raw(p.pool + (int64_t)dst * p.D, c0 * 4, pack<float>(h));
 }
 
 // Calls f with the kernel's element type, vector width and gate form as types:

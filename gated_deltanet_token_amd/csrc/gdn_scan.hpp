@@ -6,22 +6,67 @@
 
 namespace gdn {
 
-// VEC neighbouring elements in their storage type: one access of their size.
-template <typename DT, int VEC> struct alignas(sizeof(DT) * VEC) Raw {
-    DT v[VEC];
-    __device__ __forceinline__ float operator[](int e) const { return to_f32(v[e]); }
-    __device__ __forceinline__ void set(int e, float x) { v[e] = from_f32<DT>(x); }
+// VEC neighbouring elements in their storage type, as the words they are
+// loaded in (a struct of bf16 members would take a register for each).
+template <typename DT, int VEC> struct Raw {
+    static constexpr int kWords = VEC * (int)sizeof(DT) < 4 ? 1 : VEC * (int)sizeof(DT) / 4;
+    uint32_t w[kWords];
+
+    __device__ __forceinline__ float operator[](int e) const {
+        if constexpr (sizeof(DT) == 4) return __builtin_bit_cast(float, w[e]);
+        return __builtin_bit_cast(float, e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
+    }
+    // Elements e and e + 1 (VEC == 1: e alone).
+    __device__ __forceinline__ void set(int e, float a, float b) {
+        if constexpr (sizeof(DT) == 4) {
+            w[e] = __builtin_bit_cast(uint32_t, a);
+            if constexpr (VEC > 1) w[e + 1] = __builtin_bit_cast(uint32_t, b);
+        } else {
+            typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+            w[e / 2] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+        }
+    }
 };
+template <int N> struct Words {
+    typedef uint32_t type __attribute__((ext_vector_type(N)));
+};
+template <> struct Words<1> { typedef uint32_t type; };
+
 // VEC elements `bytes` behind base: 32-bit byte offsets within a tile
 // (kMaxScanWidth keeps them in range), so that the tile's start stays in scalar
 // registers.
 template <int VEC, typename DT>
 __device__ __forceinline__ Raw<DT, VEC> load_raw(const DT *base, uint32_t bytes) {
-    return *reinterpret_cast<const Raw<DT, VEC> *>(reinterpret_cast<const char *>(base) + bytes);
+    const char *p = reinterpret_cast<const char *>(base) + bytes;
+    Raw<DT, VEC> r;
+    if constexpr (VEC * sizeof(DT) == 2) {
+        r.w[0] = *reinterpret_cast<const uint16_t *>(p);
+    } else {
+        typedef typename Words<Raw<DT, VEC>::kWords>::type V;
+        const V v = *reinterpret_cast<const V *>(p);
+        __builtin_memcpy(r.w, &v, sizeof(v));
+    }
+    return r;
 }
 template <typename DT, int VEC>
-__device__ __forceinline__ void store_raw(DT *base, uint32_t bytes, const Raw<DT, VEC> &x) {
-    *reinterpret_cast<Raw<DT, VEC> *>(reinterpret_cast<char *>(base) + bytes) = x;
+__device__ __forceinline__ void store_raw(DT *base, uint32_t bytes, const Raw<DT, VEC> &r) {
+    char *p = reinterpret_cast<char *>(base) + bytes;
+    if constexpr (VEC * sizeof(DT) == 2) {
+        *reinterpret_cast<uint16_t *>(p) = (uint16_t)r.w[0];
+    } else {
+        typedef typename Words<Raw<DT, VEC>::kWords>::type V;
+        V v;
+        __builtin_memcpy(&v, r.w, sizeof(v));
+        *reinterpret_cast<V *>(p) = v;
+    }
+}
+// VEC values in type DT.
+template <typename DT, int VEC>
+__device__ __forceinline__ Raw<DT, VEC> pack(const float (&x)[VEC]) {
+    Raw<DT, VEC> r;
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2) r.set(e, x[e], x[VEC > 1 ? e + 1 : 0]);
+    return r;
 }
 template <typename DT> __device__ __forceinline__ const DT *as(const void *p, int64_t at) {
     return static_cast<const DT *>(p) + at;
@@ -30,26 +75,14 @@ template <typename DT> __device__ __forceinline__ DT *as(void *p, int64_t at) {
     return static_cast<DT *>(p) + at;
 }
 
-// Makes the compiler forget what it derived from x: gates are computed anew
-// behind this instead of being kept in registers across a barrier.
-template <typename DT, int VEC> __device__ __forceinline__ void forget(Raw<DT, VEC> &x) {
-    if constexpr (sizeof(x) % 4 == 0) {
-        uint32_t w[sizeof(x) / 4];
-        __builtin_memcpy(w, &x, sizeof(x));
-#pragma unroll
-        for (size_t i = 0; i < sizeof(x) / 4; ++i) asm volatile("" : "+v"(w[i]));
-        __builtin_memcpy(&x, w, sizeof(x));
-    } else {
-        uint32_t w = __builtin_bit_cast(uint16_t, x.v[0]);
-        asm volatile("" : "+v"(w));
-        x.v[0] = __builtin_bit_cast(DT, (uint16_t)w);
-    }
-}
-
+// Makes the compiler forget what it derived from x: what is needed behind this
+// is computed anew instead of being kept in registers across a barrier.
 template <typename DT, int VEC, int R>
-__device__ __forceinline__ void forget_all(Raw<DT, VEC> (&x)[R]) {
+__device__ __forceinline__ void forget(Raw<DT, VEC> (&x)[R]) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) forget(x[r]);
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < Raw<DT, VEC>::kWords; ++i) asm volatile("" : "+v"(x[r].w[i]));
 }
 
 // Gates of fp32 logits: e^z for z in [-110, 80] (held there outside), the
@@ -93,6 +126,16 @@ __device__ __forceinline__ float write_strength(float b, float) {
 }
 __device__ __forceinline__ float write_strength(float b, __bf16) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(b * -0x1.715476p+0f));
+}
+
+// The same with 1 - beta, for its gradient beta (1 - beta).
+__device__ __forceinline__ void write_pair(float b, float &beta, float &rest, float) {
+    sigmoid_pair<float>(-b, beta, rest);
+}
+__device__ __forceinline__ void write_pair(float b, float &beta, float &rest, __bf16) {
+    const float e = __builtin_amdgcn_exp2f(b * -0x1.715476p+0f);
+    beta = __builtin_amdgcn_rcpf(1.f + e);
+    rest = fminf(e, 0x1p127f) * beta;  // e may be infinite where beta is 0
 }
 
 // Gates of one element from what the caller passes: the decay, its complement
