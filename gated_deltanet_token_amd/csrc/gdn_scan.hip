@@ -426,12 +426,14 @@ bool scan_wants_split(int64_t nseq, int64_t tokens, int64_t ncb, bool packed, in
     return tokens > GDN_SCAN_TILE && nseq * ncb < 8 * (int64_t)cus;
 }
 
+constexpr int kForVec = 8;
 constexpr int kBackVec = 4;  // columns per thread of the bf16 backward kernel
 
 int scan_cols(int32_t D, int dtype, bool back) {
     if (dtype == 1 && back)
         return D % kBackVec == 0 ? ScanShape<__bf16, kBackVec>::kCols : ScanShape<__bf16, 1>::kCols;
-    if (dtype == 1) return D % 8 == 0 ? ScanShape<__bf16, 8>::kCols : ScanShape<__bf16, 1>::kCols;
+    if (dtype == 1)
+        return D % kForVec == 0 ? ScanShape<__bf16, kForVec>::kCols : ScanShape<__bf16, 1>::kCols;
     return D % 4 == 0 ? ScanShape<float, 4>::kCols : ScanShape<float, 1>::kCols;
 }
 
@@ -526,7 +528,7 @@ hipError_t launch_scan(const ScanParams &p, int dtype, int cus, void *ws, size_t
     ScanSplit sp;
     const hipError_t e = prepare_split(p, dtype, cus, ws, ws_bytes, false, sp, stream);
     if (e != hipSuccess) return e;
-    return with_scan_types<8>(dtype, p.D, p.b, p.flags, RunForward{p, sp, stream});
+    return with_scan_types<kForVec>(dtype, p.D, p.b, p.flags, RunForward{p, sp, stream});
 }
 
 hipError_t launch_scan_backward(const ScanParams &p, int dtype, int cus, void *ws,

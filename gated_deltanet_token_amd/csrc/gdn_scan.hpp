@@ -43,7 +43,7 @@ __device__ __forceinline__ Raw<DT, VEC> load_raw(const DT *base, uint32_t bytes)
         r.w[0] = *reinterpret_cast<const uint16_t *>(p);
     } else {
         typedef typename Words<Raw<DT, VEC>::kWords>::type V;
-        const V v = *reinterpret_cast<const V *>(p);
+        const V v = __builtin_nontemporal_load(reinterpret_cast<const V *>(p));
         __builtin_memcpy(r.w, &v, sizeof(v));
     }
     return r;
@@ -57,7 +57,7 @@ __device__ __forceinline__ void store_raw(DT *base, uint32_t bytes, const Raw<DT
         typedef typename Words<Raw<DT, VEC>::kWords>::type V;
         V v;
         __builtin_memcpy(&v, r.w, sizeof(v));
-        *reinterpret_cast<V *>(p) = v;
+        __builtin_nontemporal_store(v, reinterpret_cast<V *>(p));
     }
 }
 // VEC values in type DT.
