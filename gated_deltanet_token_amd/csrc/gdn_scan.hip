@@ -223,6 +223,10 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads), 4) void scan_backwa
             else if (p.h0)
                 h_in = p.h0[(int64_t)n * D + ch];
         }
+        // alpha and beta as fp32 for both sweeps, where they fit the registers of
+        // two workgroups per CU; else they are formed twice
+        constexpr bool HOLD = sizeof(DT) == 2 && R * VEC <= 16;
+        float al[HOLD ? R : 1][VEC], be[HOLD ? R : 1][VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             float A = 1.f, H = 0.f, K = 0.f;
@@ -231,6 +235,10 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads), 4) void scan_backwa
                 const bool in = g * R + r < left;
                 float alpha, keep, beta;
                 gates<DT, TIED, LOGITS>(a[r][e], b[r][e], alpha, keep, beta);
+                if constexpr (HOLD) {
+                    al[r][e] = alpha;
+                    be[r][e] = beta;
+                }
                 alpha = in ? alpha : 1.f;
                 H = fmaf(alpha, H, in ? beta * x[r][e] : 0.f);
                 // rows join at the far end: K = sum of dy_r times the decays up to it
@@ -289,8 +297,17 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads), 4) void scan_backwa
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 before[r] = h;
-                gates<DT, TIED, LOGITS>(a[r][e], b[r][e], alpha[r], keep[r], beta[r]);
-                if constexpr (!TIED && LOGITS) write_pair(b[r][e], beta[r], rest[r], DT());
+                if constexpr (HOLD) {
+                    alpha[r] = al[r][e];
+                    beta[r] = be[r][e];
+                    if constexpr (LOGITS) {
+                        keep[r] = TIED ? beta[r] : exp_logit(a[r][e], DT()) * alpha[r];
+                        if constexpr (!TIED) rest[r] = write_rest(b[r][e], beta[r]);
+                    }
+                } else {
+                    gates<DT, TIED, LOGITS>(a[r][e], b[r][e], alpha[r], keep[r], beta[r]);
+                    if constexpr (!TIED && LOGITS) write_pair(b[r][e], beta[r], rest[r], DT());
+                }
                 h = fmaf(alpha[r], h, beta[r] * x[r][e]);
             }
 #pragma unroll

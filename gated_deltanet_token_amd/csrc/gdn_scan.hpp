@@ -132,10 +132,14 @@ __device__ __forceinline__ float write_strength(float b, __bf16) {
 __device__ __forceinline__ void write_pair(float b, float &beta, float &rest, float) {
     sigmoid_pair<float>(-b, beta, rest);
 }
+// 1 - beta = e^-b beta of a bf16 logit.
+__device__ __forceinline__ float write_rest(float b, float beta) {
+    // e^-b may be infinite where beta is 0
+    return fminf(__builtin_amdgcn_exp2f(b * -0x1.715476p+0f), 0x1p127f) * beta;
+}
 __device__ __forceinline__ void write_pair(float b, float &beta, float &rest, __bf16) {
-    const float e = __builtin_amdgcn_exp2f(b * -0x1.715476p+0f);
-    beta = __builtin_amdgcn_rcpf(1.f + e);
-    rest = fminf(e, 0x1p127f) * beta;  // e may be infinite where beta is 0
+    beta = write_strength(b, __bf16());
+    rest = write_rest(b, beta);
 }
 
 // Gates of one element from what the caller passes: the decay, its complement
