@@ -200,15 +200,20 @@ __device__ __forceinline__ int64_t scan_block_ending(const ScanParams &p, int64_
 
 // Tiles of one sequence side by side (SPLIT kernels)
 //
-// A workgroup takes one tile. It publishes what the tile does to a state (A
-// and H of every channel) as soon as it knows it, finds the state in front of
-// it from what the tiles in front have published, and publishes the state
-// behind it. Every published state is A * (state in front) + H, formed the
-// same way by whoever forms it, so the result does not depend on how far a
+// A workgroup takes one tile: it loads it and sums it up (A and H of every
+// channel), finds the state in front of it, publishes the state behind it,
+// A * (state in front) + H, and only then walks its tokens. So a chain of tiles
+// advances by one published word per channel and tile, while all else of the
+// tiles overlaps.
+//
+// With SPLIT > 1 a tile also publishes its A and H as soon as it knows them, and
+// looks at SPLIT tiles in front of it at once for the nearest published state,
+// to carry it over the maps in between itself. Every state is formed the same
+// way by whoever forms it, so the result does not depend on how far a
 // workgroup had to look.
 //
-// A value and its presence travel in one word (all bits set: not there yet;
-// the launch's first kernel sets them), written and read by relaxed atomics of
+// A value and its presence travel in one word (all bits set: not there yet; the
+// launch's first kernel sets them), written and read by relaxed atomics of
 // device scope, so no fence orders them.
 //
 // Workgroups take the tiles of a chain in order from a counter. A tile waits
@@ -217,11 +222,12 @@ __device__ __forceinline__ int64_t scan_block_ending(const ScanParams &p, int64_
 // publishes: every wait ends.
 struct ScanSplit {
     uint32_t *ticket;  // [chains]
-    uint64_t *agg;     // [slots][width]: A low, H high
-    uint32_t *inc;     // [slots][width]
+    uint64_t *map;     // [slots][width], SPLIT > 1: A low, H high
+    uint32_t *state;   // [slots][width]
     int32_t chains;    // dense: N * column blocks, packed: column blocks
     int32_t slots;     // dense: tiles * N (tile-major), packed: floor(total / tile) + N
     int32_t width;     // columns, up to whole column blocks
+    int32_t deep;      // the kernels' SPLIT
 };
 
 constexpr uint32_t kAbsent = 0xFFFFFFFFu;
@@ -236,41 +242,54 @@ template <typename T> __device__ __forceinline__ void publish(T *p, T v) {
 template <typename T> __device__ __forceinline__ T observe(const T *p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ uint64_t scan_pair(float A, float H) {
-    return (uint64_t)scan_word(H) << 32 | scan_word(A);
+__device__ __forceinline__ void publish_state(const ScanSplit &sp, int64_t slot, int col, float x) {
+    publish(sp.state + slot * sp.width + col, scan_word(x));
+}
+__device__ __forceinline__ void publish_map(const ScanSplit &sp, int64_t slot, int col, float A,
+                                            float H) {
+    publish(sp.map + slot * sp.width + col, (uint64_t)scan_word(H) << 32 | scan_word(A));
 }
 
-// The state in front of a tile: `ahead` tiles of its sequence lie in front, at
-// slots `at`, at + step, ... (step is negative for the backward pass's order).
-// kDeep of them are read at a time.
-__device__ __forceinline__ float scan_look(const ScanSplit &sp, int64_t at, int64_t step,
-                                           int32_t ahead, int col) {
-    constexpr int kDeep = 4;
-    for (;;) {
-        uint32_t inc[kDeep];
-        uint64_t agg[kDeep];
-#pragma unroll
-        for (int j = 0; j < kDeep; ++j) {
-            const int64_t i = (at + (j < ahead ? j : ahead - 1) * step) * sp.width + col;
-            inc[j] = observe(sp.inc + i);
-            agg[j] = observe(sp.agg + i);
+// The state in front of a tile: `ahead` (at least 1) tiles of its sequence lie
+// in front, at slots `at`, at + step, ... (step is positive for the backward
+// pass, whose tiles come from the end).
+template <int SPLIT>
+__device__ __forceinline__ float find_state(const ScanSplit &sp, int64_t at, int64_t step,
+                                            int32_t ahead, int col) {
+    if constexpr (SPLIT == 1) {
+        const uint32_t *p = sp.state + at * sp.width + col;
+        for (;;) {
+            const uint32_t w = observe(p);
+            if (w != kAbsent) return __builtin_bit_cast(float, w);
+            __builtin_amdgcn_s_sleep(1);
         }
-        float c = 0.f;
-        bool found = false;
+    } else {
+        for (;;) {
+            uint32_t state[SPLIT];
+            uint64_t map[SPLIT];
 #pragma unroll
-        for (int j = kDeep - 1; j >= 0; --j) {
-            if (j >= ahead) continue;
-            if (inc[j] != kAbsent) {
-                c = __builtin_bit_cast(float, inc[j]);
-                found = true;
-            } else {
-                found &= agg[j] != ~(uint64_t)0;
-                c = fmaf(__builtin_bit_cast(float, (uint32_t)agg[j]), c,
-                         __builtin_bit_cast(float, (uint32_t)(agg[j] >> 32)));
+            for (int j = 0; j < SPLIT; ++j) {
+                const int64_t i = (at + (j < ahead ? j : ahead - 1) * step) * sp.width + col;
+                state[j] = observe(sp.state + i);
+                map[j] = observe(sp.map + i);
             }
+            float c = 0.f;
+            bool found = false;
+#pragma unroll
+            for (int j = SPLIT - 1; j >= 0; --j) {
+                if (j >= ahead) continue;
+                if (state[j] != kAbsent) {
+                    c = __builtin_bit_cast(float, state[j]);
+                    found = true;
+                } else {
+                    found &= map[j] != ~(uint64_t)0;
+                    c = fmaf(__builtin_bit_cast(float, (uint32_t)map[j]), c,
+                             __builtin_bit_cast(float, (uint32_t)(map[j] >> 32)));
+                }
+            }
+            if (found) return c;
+            __builtin_amdgcn_s_sleep(1);
         }
-        if (found) return c;
-        __builtin_amdgcn_s_sleep(1);
     }
 }
 
