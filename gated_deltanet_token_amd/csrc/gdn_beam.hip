@@ -43,15 +43,22 @@ __device__ __forceinline__ uint64_t key_of(float x, uint32_t place) {
     return ((uint64_t)ordered(x) << 32) | (uint32_t)~place;
 }
 
+// Over the wave, by DPP within rows of 16 lanes and scalar reads of the rows.
+__device__ __forceinline__ float lane_value(float x, int lane) {
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
+}
 __device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) x = fmaxf(x, __shfl_xor(x, o));
-    return x;
+    x = fmaxf(x, GDN_DPP(x, 0xB1));
+    x = fmaxf(x, GDN_DPP(x, 0x4E));
+    x = fmaxf(x, GDN_DPP(x, 0x141));
+    x = fmaxf(x, GDN_DPP(x, 0x140));
+    return fmaxf(fmaxf(lane_value(x, 0), lane_value(x, 16)),
+                 fmaxf(lane_value(x, 32), lane_value(x, 48)));
 }
 __device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o);
-    return x;
+    x = row16_sum(x);
+    return (lane_value(x, 0) + lane_value(x, 16)) + (lane_value(x, 32) + lane_value(x, 48));
 }
 
 struct PieceSum {
@@ -62,7 +69,11 @@ struct PieceSum {
 // thread's share is counted from its row's start all the same, so that equal
 // rows give equal sums bit by bit and their candidates tie.
 template <typename DT> struct __attribute__((packed, aligned(sizeof(DT)))) Eight {
-    DT v[8];
+    uint32_t w[2 * sizeof(DT)];
+    __device__ __forceinline__ float operator[](int e) const {
+        if constexpr (sizeof(DT) == 4) return __builtin_bit_cast(float, w[e]);
+        return __builtin_bit_cast(float, e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
+    }
 };
 
 // The largest o such that at least `want` of the wave's lanes hold x >= o (0 if
@@ -98,18 +109,24 @@ __global__ __launch_bounds__(kThreads) void beam_piece_kernel(const DT *logits, 
     // element e of vector j: the piece's (j * 256 + tid) * 8 + e
     float v[VECS][8], vtop[VECS];
     float top = -__builtin_inff();
+    if (here == kPiece) {  // all loads before the first use
+        Eight<DT> q[VECS];
 #pragma unroll
-    for (int j = 0; j < VECS; ++j) {
-        const int at = (j * kThreads + tid) * 8;
-        if (at + 8 <= here) {
-            const Eight<DT> q = *reinterpret_cast<const Eight<DT> *>(from + at);
+        for (int j = 0; j < VECS; ++j)
+            q[j] = *reinterpret_cast<const Eight<DT> *>(from + (j * kThreads + tid) * 8);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[j][e] = to_f32(q.v[e]);
-        } else {
+        for (int j = 0; j < VECS; ++j)
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[j][e] = at + e < here ? to_f32(from[at + e]) : -__builtin_inff();
-        }
+            for (int e = 0; e < 8; ++e) v[j][e] = q[j][e];
+    } else {
+#pragma unroll
+        for (int j = 0; j < VECS; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int at = (j * kThreads + tid) * 8 + e;
+                const float x = to_f32(from[at < here ? at : here - 1]);
+                v[j][e] = at < here ? x : -__builtin_inff();
+            }
     }
 #pragma unroll
     for (int j = 0; j < VECS; ++j) {
@@ -463,7 +480,11 @@ hipError_t launch_beam(const BeamParams &p, int dtype, void *ws, hipStream_t str
 #undef GDN_BEAM_LAUNCH
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (np * p.W * p.W <= 1024)
+    // a wave per beam where that is enough of them: their sums take the longest
+    if (p.W > 4 && p.W <= 8 && np * p.W * p.W <= 2048)
+        hipLaunchKernelGGL((beam_join_kernel<512, 4>), dim3((unsigned)p.B), dim3(512), 0, stream,
+                           p, (int)np, sums, best);
+    else if (np * p.W * p.W <= 1024)
         hipLaunchKernelGGL((beam_join_kernel<256, 4>), dim3((unsigned)p.B), dim3(256), 0, stream,
                            p, (int)np, sums, best);
     else
