@@ -89,7 +89,7 @@ __device__ __forceinline__ uint32_t wave_bound(uint32_t x, int want, int low) {
 
 // Logits per workgroup: VECS times 8 per thread.
 template <typename DT, int VECS>
-__global__ __launch_bounds__(kThreads) void beam_piece_kernel(const DT *logits, int64_t V, int W,
+__global__ __launch_bounds__(kThreads, 8) void beam_piece_kernel(const DT *logits, int64_t V, int W,
                                                               int npieces, PieceSum *sums,
                                                               uint64_t *best) {
     constexpr int kPiece = VECS * 8 * kThreads;
@@ -177,17 +177,20 @@ __global__ __launch_bounds__(kThreads) void beam_piece_kernel(const DT *logits, 
     // of the (negative) or the only (positive) pattern with that upper half.
     const float bound = unordered(ob);
     const bool picky = some && ob > ordered(-__builtin_inff());
-    if (picky && top >= bound) {
+    const bool few = here <= kList;  // all of them fit the list
+    if (picky ? top >= bound : few) {
 #pragma unroll
         for (int j = 0; j < VECS; ++j) {
-            if (!(vtop[j] >= bound)) continue;
+            if (picky && !(vtop[j] >= bound)) continue;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (v[j][e] >= bound) {  // elements past the end are -inf
+            for (int e = 0; e < 8; ++e) {
+                const int at = (j * kThreads + tid) * 8 + e;
+                // places past the end are -inf, below any bound but this one
+                if (picky ? v[j][e] >= bound : at < here && v[j][e] == v[j][e]) {
                     const int i = atomicAdd(&s_count, 1);
-                    if (i < kList)
-                        s_list[i] = key_of(v[j][e], first + (j * kThreads + tid) * 8 + e);
+                    if (i < kList) s_list[i] = key_of(v[j][e], first + at);
                 }
+            }
         }
     }
     __syncthreads();
@@ -198,7 +201,7 @@ __global__ __launch_bounds__(kThreads) void beam_piece_kernel(const DT *logits, 
         sums[blockIdx.x] = PieceSum{all != all ? all : m, all};
     }
     const int count = s_count;
-    if (picky && count <= kList) {
+    if ((picky || few) && count <= kList) {
         for (int i = tid; i < count; i += kThreads) {
             const uint64_t k = s_list[i];
             int rank = 0;
@@ -208,18 +211,15 @@ __global__ __launch_bounds__(kThreads) void beam_piece_kernel(const DT *logits, 
         if (tid >= count && tid < W) out[tid] = 0;
     } else if (!some) {
         if (tid < W) out[tid] = tid < here ? key_of(-__builtin_inff(), first + tid) : 0;
-    } else {  // W rounds, each the best key below the last one
+    } else {  // W rounds, each the best key below the last one; the logits from memory again
         uint64_t last = ~(uint64_t)0;
         for (int k = 0; k < W; ++k) {
             uint64_t c = 0;
-#pragma unroll
-            for (int j = 0; j < VECS; ++j)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int at = (j * kThreads + tid) * 8 + e;
-                    const uint64_t x = key_of(v[j][e], first + at);
-                    if (at < here && v[j][e] == v[j][e] && x < last && x > c) c = x;
-                }
+            for (int i = tid; i < here; i += kThreads) {
+                const float l = to_f32(from[i]);
+                const uint64_t x = key_of(l, first + i);
+                if (l == l && x < last && x > c) c = x;
+            }
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) {
                 const uint64_t x = __shfl_xor(c, o);
