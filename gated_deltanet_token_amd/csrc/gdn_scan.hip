@@ -472,6 +472,22 @@ int scan_cols(int32_t D, int dtype, bool back) {
     return D % 4 == 0 ? ScanShape<float, 4>::kCols : ScanShape<float, 1>::kCols;
 }
 
+}  // namespace
+
+size_t scan_workspace_bytes(int64_t nseq, int64_t tokens, int32_t D, int dtype, bool packed,
+                            int cus) {
+    int64_t most = 0;  // of the forward and the backward call
+    for (const bool back : {false, true}) {
+        const int cols = scan_cols(D, dtype, back);
+        const ScanLayout l = scan_layout(nseq, tokens, D, cols, packed);
+        if (scan_wants_split(nseq, tokens, l.width / cols, packed, cus) && l.bytes > most)
+            most = l.bytes;
+    }
+    return (size_t)most;
+}
+
+namespace {
+
 // Fills sp and clears the workspace when the call is to be cut; sp.slots is 0
 // when not.
 hipError_t prepare_split(const ScanParams &p, int dtype, int cus, void *ws, size_t ws_bytes,
@@ -481,7 +497,7 @@ hipError_t prepare_split(const ScanParams &p, int dtype, int cus, void *ws, size
     const int64_t tokens = packed ? p.total : p.T;
     const int cols = scan_cols(p.D, dtype, back);
     const ScanLayout l = scan_layout(p.N, tokens, p.D, cols, packed);
-    if (!ws || ws_bytes < (size_t)l.bytes ||
+    if (!ws || ws_bytes < scan_workspace_bytes(p.N, tokens, p.D, dtype, packed, cus) ||
         !scan_wants_split(p.N, tokens, l.width / cols, packed, cus))
         return hipSuccess;
     char *base = static_cast<char *>(ws);
@@ -553,18 +569,6 @@ struct RunDecode {
 };
 
 }  // namespace
-
-size_t scan_workspace_bytes(int64_t nseq, int64_t tokens, int32_t D, int dtype, bool packed,
-                            int cus) {
-    int64_t most = 0;  // of the forward and the backward call
-    for (const bool back : {false, true}) {
-        const int cols = scan_cols(D, dtype, back);
-        const ScanLayout l = scan_layout(nseq, tokens, D, cols, packed);
-        if (scan_wants_split(nseq, tokens, l.width / cols, packed, cus) && l.bytes > most)
-            most = l.bytes;
-    }
-    return (size_t)most;
-}
 
 hipError_t launch_scan(const ScanParams &p, int dtype, int cus, void *ws, size_t ws_bytes,
                        hipStream_t stream) {

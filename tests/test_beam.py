@@ -182,3 +182,33 @@ def test_gather_refuses(gdn):
     src = torch.zeros(4, 4, device=DEV)
     with pytest.raises(gdn.GDNError):
         gdn.gdn_gather_states(src, idx, out=src[:2])
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [20000, 8200])
+def test_masks_over_several_pieces(gdn, dt, V):
+    """Rows with fewer tokens left than beams, in one piece or spread; pieces of nothing but -inf;
+    more equal values than the ranked list holds."""
+    W = 6
+    g = torch.Generator().manual_seed(V)
+    scores = torch.randn(2, W, generator=g)
+    x = torch.full((2, W, V), -math.inf)
+    for b in range(2):
+        for w in range(W):
+            at = torch.randperm(V, generator=g)[:w + 1]
+            x[b, w, at] = torch.randn(w + 1, generator=g)
+    check(gdn, x.to(DT[dt]), scores)
+    x[1, 2, V // 2:] = 1.0  # equal values, far more than fit
+    x[0, :, 3000:] = -2.0
+    check(gdn, x.to(DT[dt]), scores)
+    check(gdn, x.to(DT[dt]), scores, torch.ones(2, W, dtype=torch.uint8), V - 1)
+
+
+@gpu
+@pytest.mark.parametrize("W,V", [(32, 70000), (16, 131072), (8, 300001), (3, 2100000)])
+def test_many_candidates(gdn, W, V):
+    """More pieces and beams than the joining threads hold."""
+    g = torch.Generator(device=DEV).manual_seed(V)
+    x = (torch.randn(1, W, V, generator=g, device=DEV) * 3).bfloat16().cpu()
+    check(gdn, x, torch.randn(1, W, generator=torch.Generator().manual_seed(W)))

@@ -382,3 +382,43 @@ def test_offsets_past_32_bits(gdn):
     scale = e.max() * K * U32 * 2 + half_step(torch.bfloat16) * h.abs().max() * 2
     assert (out[0, lo:].double() - o2[0].double()).abs().max() <= scale
     assert (fin - f2).abs().max() <= scale
+
+
+MANY = [  # B, T, D, dtype, tied: chains of one published word; enough sequences for none
+    (4, 400, 2048, "bf16", False), (3, 385, 1600, "f32", True), (2, 300, 1999, "bf16", True),
+    (2, 260, 2001, "f32", False), (2100, 130, 8, "bf16", False), (130, 257, 1024, "f32", False),
+]
+
+
+@gpu
+@pytest.mark.parametrize("case", MANY, ids=str)
+def test_many_chains(gdn, case):
+    """Forward and backward where the call has many (sequence, column block) pairs: the same bits
+    with and without a workspace, and the oracle on some sequences and columns."""
+    B, T, D, dt, tied = case
+    dtype = DT[dt]
+    g = torch.Generator(device=DEV).manual_seed(T + D)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    x, dy = r(B, T, D).to(dtype), r(B, T, D).to(dtype)
+    a, b = (r(B, T, D) * 2 - 3).to(dtype), None if tied else r(B, T, D).to(dtype)
+    s, dh = r(B, D), r(B, D)
+    pre = torch.empty(gdn.prefix_state_rows(B, T, 1, False), D, device=DEV)
+    kw = dict(flags=2, prefix_states=pre, prefix_interval=1)
+    out, fin = gdn.gdn_scan_prefill(x, a, b, s, **kw)
+    kept = pre.clone()
+    grads = gdn.gdn_scan_backward(dy, x, a, b, s, dfinal=dh, **kw)
+    out2, fin2 = gdn.gdn_scan_prefill(x, a, b, s, workspace=None, **kw)
+    assert torch.equal(out, out2) and torch.equal(fin, fin2) and torch.equal(pre, kept)
+    for p, q in zip(grads, gdn.gdn_scan_backward(dy, x, a, b, s, dfinal=dh, workspace=None, **kw)):
+        assert p is None or torch.equal(p, q)
+    cols = torch.tensor(sorted({0, 1, D // 2, D - 2, D - 1, min(D - 1, 127), min(D - 1, 128)}))
+    for n in sorted({0, B // 2, B - 1}):
+        cut = lambda t: None if t is None else t[n].cpu()[..., cols]  # noqa: E731
+        h, e = scan64(cut(x), cut(a), cut(b), cut(s), True)
+        assert_scan_close(cut(out), h, e, dtype, "out")
+        assert_scan_close(cut(fin), h[-1], e[-1], torch.float32, "final")
+        want, err = scan_backward64(cut(dy), cut(x), cut(a), cut(b), cut(s), cut(dh), True)
+        for name, got in zip(("dx", "da", "db"), grads):
+            if got is not None:
+                assert_scan_close(cut(got), want[name], err[name], dtype, name)
+        assert_scan_close(cut(grads[3]), want["dh0"], err["dh0"], torch.float32, "dh0")
