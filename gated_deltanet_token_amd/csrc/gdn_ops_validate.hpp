@@ -148,7 +148,7 @@ static inline int64_t norm_groups(int32_t D, int32_t group) {
 static inline gdn_status_t check_norm_shape(int64_t rows, int32_t D, gdn_dtype_t dtype,
                                             float eps, int64_t &n) {
     if (rows < 0 || rows > kMaxGrid || D < 1) return GDN_ERR_BAD_SHAPE;
-    if (!(eps > 0.f) || eps > 3.0e38f) return GDN_ERR_BAD_SHAPE;
+    if (!(eps >= 0x1p-126f) || eps > 3.0e38f) return GDN_ERR_BAD_SHAPE;  // no denormals
     if (D > kMaxNormWidth || !known_dtype(dtype)) return GDN_ERR_UNSUPPORTED;
     n = bytes_of(rows, D, dtype == GDN_BF16 ? 2 : 4);
     return n < 0 ? GDN_ERR_BAD_SHAPE : GDN_OK;

@@ -28,22 +28,22 @@ struct ScanTile {
 };
 template <bool BACK>
 __device__ __forceinline__ ScanTile take_tile(const ScanParams &p, const ScanSplit &sp, int ncb,
-                                              int *s_ticket) {
+                                              int *s_take) {
     const int chain = blockIdx.x % sp.chains;
-    if (threadIdx.x == 0)
-        *s_ticket = (int)__hip_atomic_fetch_add(sp.ticket + chain, 1u, __ATOMIC_RELAXED,
+    if (threadIdx.x == 0) {
+        s_take[0] = (int)__hip_atomic_fetch_add(sp.ticket + chain, 1u, __ATOMIC_RELAXED,
                                                 __HIP_MEMORY_SCOPE_AGENT);
+        s_take[1] = 0;
+    }
     __syncthreads();
-    int64_t k = __builtin_amdgcn_readfirstlane(*s_ticket);  // uniform, and known to be
+    int64_t k = __builtin_amdgcn_readfirstlane(s_take[0]);  // uniform, and known to be
     ScanTile t;
     if (p.cu) {
         if (BACK) k = sp.slots - 1 - k;
         t.cb = chain;
         t.slot = k;
-        t.n = scan_slot_sequence(p, k);
-        int64_t base = p.cu[t.n];
-        base = base < 0 ? 0 : (base > p.total ? p.total : base);
-        t.tile = k - (base / GDN_SCAN_TILE + t.n);
+        t.n = scan_slot_sequence(p, k, s_take + 1);
+        t.tile = k - scan_first_slot(p, t.n);
     } else {
         if (BACK) k = sp.slots / p.N - 1 - k;
         t.n = chain / ncb;
@@ -63,9 +63,9 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_forward_k
     constexpr int G = Sh::kGroups, C = Sh::kCols, R = Sh::kPer;
     __shared__ float s_a[G][C], s_h[G][C];
 
-    __shared__ int s_ticket;
+    __shared__ int s_take[2];
     ScanTile mine{(int)(blockIdx.x / ncb), (int)(blockIdx.x % ncb), 0, 0};
-    if constexpr (SPLIT > 0) mine = take_tile<false>(p, sp, ncb, &s_ticket);
+    if constexpr (SPLIT > 0) mine = take_tile<false>(p, sp, ncb, s_take);
     const int n = mine.n, cb = mine.cb;
     const int tid = threadIdx.x, g = tid / Sh::kLanes, l = tid % Sh::kLanes;
     const int D = p.D, c0 = cb * C + l * VEC;
@@ -178,9 +178,9 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads), 4) void scan_backwa
     constexpr int G = Sh::kGroups, C = Sh::kCols, R = Sh::kPer;
     __shared__ float s_a[G][C], s_h[G][C], s_k[G][C];
 
-    __shared__ int s_ticket;
+    __shared__ int s_take[2];
     ScanTile mine{(int)(blockIdx.x / ncb), (int)(blockIdx.x % ncb), 0, 0};
-    if constexpr (SPLIT > 0) mine = take_tile<true>(p, sp, ncb, &s_ticket);
+    if constexpr (SPLIT > 0) mine = take_tile<true>(p, sp, ncb, s_take);
     const int n = mine.n, cb = mine.cb;
     const int tid = threadIdx.x, g = tid / Sh::kLanes, l = tid % Sh::kLanes;
     const int D = p.D, c0 = cb * C + l * VEC;

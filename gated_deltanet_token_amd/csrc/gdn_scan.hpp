@@ -293,21 +293,25 @@ __device__ __forceinline__ float find_state(const ScanSplit &sp, int64_t at, int
     }
 }
 
-// Which tile a packed batch's slot is: sequence n owns the slots from
+// First slot of sequence n of a packed batch: it owns the slots from
 // floor(start / tile) + n on, as many as it has tiles, and at least one (a
 // sequence without tokens has its state handed on there).
-__device__ __forceinline__ int scan_slot_sequence(const ScanParams &p, int64_t slot) {
-    int lo = 0, hi = p.N - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        int64_t base = p.cu[mid];
-        base = base < 0 ? 0 : (base > p.total ? p.total : base);
-        if (base / GDN_SCAN_TILE + mid <= slot)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    return lo;
+__device__ __forceinline__ int64_t scan_first_slot(const ScanParams &p, int n) {
+    int64_t base = p.cu[n];
+    base = base < 0 ? 0 : (base > p.total ? p.total : base);
+    return base / GDN_SCAN_TILE + n;
+}
+
+// The sequence of a slot: the last one that starts at or before it, looked for
+// by the whole workgroup at once (a binary search would be a chain of loads in
+// front of every tile). s_seq starts at 0, and every thread reaches this call.
+__device__ __forceinline__ int scan_slot_sequence(const ScanParams &p, int64_t slot, int *s_seq) {
+    int last = 0;
+    for (int n = threadIdx.x; n < p.N; n += blockDim.x)
+        if (scan_first_slot(p, n) <= slot) last = n;
+    if (last > 0) atomicMax(s_seq, last);
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(*s_seq);
 }
 
 }  // namespace gdn

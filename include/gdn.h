@@ -440,8 +440,9 @@ size_t gdn_scan_workspace_size(int32_t num_seqs, int64_t tokens, int32_t D, gdn_
  *            columns (G = ceil(D / 128)); others: GDN_ERR_UNSUPPORTED.
  *
  * The sum, the mean and y are fp32; y is formed from the unrounded sum, and
- * out8 from the unrounded y. Sizes: rows >= 0, 1 <= D <= 16384, eps > 0. At
- * least one of out and out8. A NaN or Inf in a row makes NaN in that row.
+ * out8 from the unrounded y. Sizes: rows >= 0, 1 <= D <= 16384, eps a
+ * normal fp32 number. At least one of out and out8. A NaN or Inf in a row, or
+ * squares whose sum passes fp32's range, make NaN of that row.
  */
 gdn_status_t gdn_rms_norm(const void *x, const void *residual, const void *weight,
                           void *residual_out, void *out, void *out8, float *scales,

@@ -422,3 +422,19 @@ def test_many_chains(gdn, case):
             if got is not None:
                 assert_scan_close(cut(got), want[name], err[name], dtype, name)
         assert_scan_close(cut(grads[3]), want["dh0"], err["dh0"], torch.float32, "dh0")
+
+
+@gpu
+def test_debug_checks_offsets(gdn, monkeypatch):
+    """GDN_DEBUG=1: malformed offsets are refused before any launch."""
+    x = torch.zeros(300, 8, device=DEV)
+    monkeypatch.setenv("GDN_DEBUG", "1")
+    for cu in ([0, 200, 100], [1, 100, 300], [0, 100, 299], [0, 301, 300]):
+        c = torch.tensor(cu, dtype=torch.int32, device=DEV)
+        with pytest.raises(gdn.GDNError):
+            gdn.gdn_scan_varlen_prefill(x, x, x, c)
+        with pytest.raises(gdn.GDNError):
+            gdn.gdn_scan_varlen_backward(x, x, x, x, c, prefix_states=torch.zeros(4, 8, device=DEV),
+                                         prefix_interval=2)
+    c = torch.tensor([0, 100, 300], dtype=torch.int32, device=DEV)
+    gdn.gdn_scan_varlen_prefill(x, x, x, c)
