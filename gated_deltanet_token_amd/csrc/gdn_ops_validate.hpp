@@ -69,7 +69,7 @@ static inline gdn_status_t check_scan_common(const ScanArgs &s, int64_t &nx, int
     // workgroups: a tile of tokens (or a piece of one) by at least 64 channels
     const int64_t cb = (s.D + 63) / 64;
     int64_t wgs = s.tokens / GDN_SCAN_TILE + s.nstates;
-    if (!mul_ok(wgs, cb) || wgs > kMaxGrid) return GDN_ERR_BAD_SHAPE;
+    if (!mul_ok(wgs, cb + 8) || wgs > kMaxGrid) return GDN_ERR_BAD_SHAPE;
     if (s.tokens > 0 && (!s.x || !s.a)) return GDN_ERR_NULL_POINTER;
     if (s.cu_count > 0 && !s.cu) return GDN_ERR_NULL_POINTER;
     if (s.ws_bytes > (size_t)INT64_MAX) return GDN_ERR_BAD_SHAPE;

@@ -20,8 +20,8 @@ namespace gdn {
 
 namespace {
 
-// The tile that a workgroup of a SPLIT launch takes: its sequence, column block
-// and tile (whose count is `tiles`; a tile at or past it does not exist).
+// The tile that a workgroup of a SPLIT launch takes: its sequence (-1: no tile),
+// column block and tile, which may lie past the sequence's last one.
 struct ScanTile {
     int n, cb;
     int64_t slot, tile;
@@ -29,7 +29,8 @@ struct ScanTile {
 template <bool BACK>
 __device__ __forceinline__ ScanTile take_tile(const ScanParams &p, const ScanSplit &sp, int ncb,
                                               int *s_take) {
-    const int chain = blockIdx.x % sp.chains;
+    const int chain = sp.runs.chain(blockIdx.x % sp.runs.grid);
+    if (chain < 0) return ScanTile{-1, 0, 0, 0};
     if (threadIdx.x == 0) {
         s_take[0] = (int)__hip_atomic_fetch_add(sp.ticket + chain, 1u, __ATOMIC_RELAXED,
                                                 __HIP_MEMORY_SCOPE_AGENT);
@@ -64,8 +65,10 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_forward_k
     __shared__ float s_a[G][C], s_h[G][C];
 
     __shared__ int s_take[2];
-    ScanTile mine{(int)(blockIdx.x / ncb), (int)(blockIdx.x % ncb), 0, 0};
+    const int pair = SPLIT > 0 ? 0 : sp.runs.chain(blockIdx.x);
+    ScanTile mine{pair / ncb, pair % ncb, 0, 0};
     if constexpr (SPLIT > 0) mine = take_tile<false>(p, sp, ncb, s_take);
+    if (SPLIT > 0 ? mine.n < 0 : pair < 0) return;
     const int n = mine.n, cb = mine.cb;
     const int tid = threadIdx.x, g = tid / Sh::kLanes, l = tid % Sh::kLanes;
     const int D = p.D, c0 = cb * C + l * VEC;
@@ -179,8 +182,10 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads), 4) void scan_backwa
     __shared__ float s_a[G][C], s_h[G][C], s_k[G][C];
 
     __shared__ int s_take[2];
-    ScanTile mine{(int)(blockIdx.x / ncb), (int)(blockIdx.x % ncb), 0, 0};
+    const int pair = SPLIT > 0 ? 0 : sp.runs.chain(blockIdx.x);
+    ScanTile mine{pair / ncb, pair % ncb, 0, 0};
     if constexpr (SPLIT > 0) mine = take_tile<true>(p, sp, ncb, s_take);
+    if (SPLIT > 0 ? mine.n < 0 : pair < 0) return;
     const int n = mine.n, cb = mine.cb;
     const int tid = threadIdx.x, g = tid / Sh::kLanes, l = tid % Sh::kLanes;
     const int D = p.D, c0 = cb * C + l * VEC;
@@ -497,16 +502,19 @@ hipError_t prepare_split(const ScanParams &p, int dtype, int cus, void *ws, size
     const int64_t tokens = packed ? p.total : p.T;
     const int cols = scan_cols(p.D, dtype, back);
     const ScanLayout l = scan_layout(p.N, tokens, p.D, cols, packed);
+    const int64_t ncb = l.width / cols;
+    sp.runs = XcdRuns::make(p.N * ncb, ncb);  // one workgroup each, unless cut
     if (!ws || ws_bytes < scan_workspace_bytes(p.N, tokens, p.D, dtype, packed, cus) ||
-        !scan_wants_split(p.N, tokens, l.width / cols, packed, cus))
+        !scan_wants_split(p.N, tokens, ncb, packed, cus))
         return hipSuccess;
+    sp.runs = XcdRuns::make(l.chains, ncb);
+    sp.per_chain = l.slots * ncb / l.chains;
     char *base = static_cast<char *>(ws);
     sp.ticket = reinterpret_cast<uint32_t *>(base);
     sp.map = reinterpret_cast<uint64_t *>(base + l.words_at);
     sp.state = reinterpret_cast<uint32_t *>(base + l.words_at) +
                (l.deep > 1 ? 2 * l.slots * l.width : 0);
     sp.deep = l.deep;
-    sp.chains = (int32_t)l.chains;
     sp.slots = (int32_t)l.slots;
     sp.width = (int32_t)l.width;
     const int64_t total = (l.bytes + 15) / 16, wgs = (total + 255) / 256;
@@ -522,16 +530,16 @@ struct RunForward {
     template <typename DT, int VEC, bool TIED, bool LOGITS> hipError_t run() const {
         const int ncb = column_blocks<DT, VEC>(p.D);
         const dim3 block(ScanShape<DT, VEC>::kThreads);
-        const dim3 tiles((unsigned)((int64_t)sp.slots * ncb));
+        const dim3 grid(sp.slots > 0 ? (unsigned)(sp.per_chain * sp.runs.grid) : sp.runs.grid);
         if (sp.slots > 0 && sp.deep > 1)
-            hipLaunchKernelGGL((scan_forward_kernel<DT, VEC, TIED, LOGITS, kDeep>), tiles, block, 0,
+            hipLaunchKernelGGL((scan_forward_kernel<DT, VEC, TIED, LOGITS, kDeep>), grid, block, 0,
                                stream, p, ncb, sp);
         else if (sp.slots > 0)
-            hipLaunchKernelGGL((scan_forward_kernel<DT, VEC, TIED, LOGITS, 1>), tiles, block, 0,
+            hipLaunchKernelGGL((scan_forward_kernel<DT, VEC, TIED, LOGITS, 1>), grid, block, 0,
                                stream, p, ncb, sp);
         else
-            hipLaunchKernelGGL((scan_forward_kernel<DT, VEC, TIED, LOGITS, 0>),
-                               dim3((unsigned)(p.N * ncb)), block, 0, stream, p, ncb, sp);
+            hipLaunchKernelGGL((scan_forward_kernel<DT, VEC, TIED, LOGITS, 0>), grid, block, 0,
+                               stream, p, ncb, sp);
         return hipGetLastError();
     }
 };
@@ -543,16 +551,16 @@ struct RunBackward {
     template <typename DT, int VEC, bool TIED, bool LOGITS> hipError_t run() const {
         const int ncb = column_blocks<DT, VEC>(p.D);
         const dim3 block(ScanShape<DT, VEC>::kThreads);
-        const dim3 tiles((unsigned)((int64_t)sp.slots * ncb));
+        const dim3 grid(sp.slots > 0 ? (unsigned)(sp.per_chain * sp.runs.grid) : sp.runs.grid);
         if (sp.slots > 0 && sp.deep > 1)
-            hipLaunchKernelGGL((scan_backward_kernel<DT, VEC, TIED, LOGITS, kDeep>), tiles, block, 0,
+            hipLaunchKernelGGL((scan_backward_kernel<DT, VEC, TIED, LOGITS, kDeep>), grid, block, 0,
                                stream, p, ncb, sp);
         else if (sp.slots > 0)
-            hipLaunchKernelGGL((scan_backward_kernel<DT, VEC, TIED, LOGITS, 1>), tiles, block, 0,
+            hipLaunchKernelGGL((scan_backward_kernel<DT, VEC, TIED, LOGITS, 1>), grid, block, 0,
                                stream, p, ncb, sp);
         else
-            hipLaunchKernelGGL((scan_backward_kernel<DT, VEC, TIED, LOGITS, 0>),
-                               dim3((unsigned)(p.N * ncb)), block, 0, stream, p, ncb, sp);
+            hipLaunchKernelGGL((scan_backward_kernel<DT, VEC, TIED, LOGITS, 0>), grid, block, 0,
+                               stream, p, ncb, sp);
         return hipGetLastError();
     }
 };

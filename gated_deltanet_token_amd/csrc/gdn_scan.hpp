@@ -3,6 +3,7 @@
 #pragma once
 #include "gdn_device.hpp"
 #include "gdn_ops_launch.hpp"
+#include "gdn_xcd.hpp"
 
 namespace gdn {
 
@@ -224,10 +225,11 @@ struct ScanSplit {
     uint32_t *ticket;  // [chains]
     uint64_t *map;     // [slots][width], SPLIT > 1: A low, H high
     uint32_t *state;   // [slots][width]
-    int32_t chains;    // dense: N * column blocks, packed: column blocks
+    XcdRuns runs;      // chains: N * column blocks (dense) or column blocks (packed)
     int32_t slots;     // dense: tiles * N (tile-major), packed: floor(total / tile) + N
     int32_t width;     // columns, up to whole column blocks
     int32_t deep;      // the kernels' SPLIT
+    int64_t per_chain; // workgroups that take a chain's tiles
 };
 
 constexpr uint32_t kAbsent = 0xFFFFFFFFu;
