@@ -65,11 +65,17 @@ template <int TPR, typename Op> __device__ __forceinline__ float row_reduce(floa
     return x;
 }
 
-// 8 elements at p: one or two 16-byte accesses, or (rows that do not start on
-// 16 bytes) element by element up to `left` of them. ONCE: non-temporal, for
+// 8 elements at p: one or two 16-byte accesses, or element by element where only
+// `left` of them are the row's. ONCE: non-temporal, for
 // rows that are touched once. Wide rows gain from it (16,384 x 5,120: 112
 // against 118 us), narrow ones lose (196,608 x 128: 15.9 against 14.7 us).
-template <typename V, bool ONCE> __device__ __forceinline__ V take(const V *p) {
+// Rows that do not start on 16 bytes (VEC false) are read and written by the
+// same accesses without that alignment and hint.
+typedef __bf16 bf16x8_any __attribute__((ext_vector_type(8), aligned(2)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+
+template <bool ONCE, typename V> __device__ __forceinline__ V take(const V *p) {
     if constexpr (ONCE) return __builtin_nontemporal_load(p);
     return *p;
 }
@@ -79,22 +85,44 @@ template <bool ONCE, typename V> __device__ __forceinline__ void give(V v, V *p)
     else
         *p = v;
 }
+template <bool ONCE, typename V8>
+__device__ __forceinline__ void load_wide(const __bf16 *p, float (&x)[8]) {
+    const V8 v = take<ONCE>(reinterpret_cast<const V8 *>(p));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = (float)v[e];
+}
+template <bool ONCE, typename V4>
+__device__ __forceinline__ void load_wide(const float *p, float (&x)[8]) {
+    const V4 a = take<ONCE>(reinterpret_cast<const V4 *>(p));
+    const V4 b = take<ONCE>(reinterpret_cast<const V4 *>(p) + 1);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        x[e] = a[e];
+        x[e + 4] = b[e];
+    }
+}
+template <bool ONCE, typename V8>
+__device__ __forceinline__ void store_wide(__bf16 *p, const float (&x)[8]) {
+    V8 v;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = (__bf16)x[e];
+    give<ONCE>(v, reinterpret_cast<V8 *>(p));
+}
+template <bool ONCE, typename V4>
+__device__ __forceinline__ void store_wide(float *p, const float (&x)[8]) {
+    give<ONCE>(V4{x[0], x[1], x[2], x[3]}, reinterpret_cast<V4 *>(p));
+    give<ONCE>(V4{x[4], x[5], x[6], x[7]}, reinterpret_cast<V4 *>(p) + 1);
+}
+template <typename DT> struct Wide;
+template <> struct Wide<__bf16> { using on16 = bf16x8; using any = bf16x8_any; };
+template <> struct Wide<float> { using on16 = f32x4; using any = f32x4_any; };
+
 template <typename DT, bool VEC, bool ONCE>
 __device__ __forceinline__ void load8(const DT *p, int left, float (&x)[8]) {
     if constexpr (VEC) {
-        if constexpr (sizeof(DT) == 2) {
-            const bf16x8 v = take<bf16x8, ONCE>(reinterpret_cast<const bf16x8 *>(p));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = (float)v[e];
-        } else {
-            const f32x4 a = take<f32x4, ONCE>(reinterpret_cast<const f32x4 *>(p));
-            const f32x4 b = take<f32x4, ONCE>(reinterpret_cast<const f32x4 *>(p) + 1);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[e] = a[e];
-                x[e + 4] = b[e];
-            }
-        }
+        load_wide<ONCE, typename Wide<DT>::on16>(p, x);
+    } else if (left >= 8) {
+        load_wide<false, typename Wide<DT>::any>(p, x);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = e < left ? to_f32(p[e]) : 0.f;
@@ -103,15 +131,9 @@ __device__ __forceinline__ void load8(const DT *p, int left, float (&x)[8]) {
 template <typename DT, bool VEC, bool ONCE>
 __device__ __forceinline__ void store8(DT *p, int left, const float (&x)[8]) {
     if constexpr (VEC) {
-        if constexpr (sizeof(DT) == 2) {
-            bf16x8 v;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = (__bf16)x[e];
-            give<ONCE>(v, reinterpret_cast<bf16x8 *>(p));
-        } else {
-            give<ONCE>(f32x4{x[0], x[1], x[2], x[3]}, reinterpret_cast<f32x4 *>(p));
-            give<ONCE>(f32x4{x[4], x[5], x[6], x[7]}, reinterpret_cast<f32x4 *>(p) + 1);
-        }
+        store_wide<ONCE, typename Wide<DT>::on16>(p, x);
+    } else if (left >= 8) {
+        store_wide<false, typename Wide<DT>::any>(p, x);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -129,6 +151,8 @@ __device__ __forceinline__ void store8_e4m3(uint8_t *p, int left, const float (&
     hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[6], x[7], hi, true);
     if constexpr (VEC) {
         give<ONCE>(u32x2{(uint32_t)lo, (uint32_t)hi}, reinterpret_cast<u32x2 *>(p));
+    } else if (left >= 8) {
+        *reinterpret_cast<u32x2_any *>(p) = u32x2_any{(uint32_t)lo, (uint32_t)hi};
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
