@@ -152,23 +152,26 @@ __global__ __launch_bounds__(kThreads, 8) void beam_piece_kernel(const DT *logit
     }
     uint64_t *out = best + (int64_t)blockIdx.x * W;
     const bool some = m > -__builtin_inff();
-    // The sum of e^(l - m): l - m first, for the terms that count are near 0
-    // there, so that no rounding is common to all of them, and the lowest finite
-    // values neither overflow nor drop out of a row that holds nothing else. A
-    // NaN makes it NaN, and so does +inf, which is m then.
+    // The sum of e^(l - m) as 2^(l log2e - c), c the rounded m log2e. The terms
+    // that count have exponents near 0, so their own roundings are small; what c is
+    // off is common to all of them and taken out at the end. A NaN makes the sum
+    // NaN. Extreme rows (nothing but -inf, the lowest finite values, +inf) are
+    // summed from memory by l - m, which neither overflows for finite m nor hides
+    // a NaN or +inf: those make it NaN.
     float sum = 0.f;
-    if (some) {
+    if (fabsf(m) <= 1e38f) {
+        const float c = m * kLog2e;
 #pragma unroll
         for (int j = 0; j < VECS; ++j)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                sum += __builtin_amdgcn_exp2f((v[j][e] - m) * kLog2e);
+                sum += __builtin_amdgcn_exp2f(fmaf(v[j][e], kLog2e, -c));
+        sum *= __builtin_amdgcn_exp2f(-fmaf(m, kLog2e, -c));
     } else {
-#pragma unroll
-        for (int j = 0; j < VECS; ++j)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (v[j][e] != v[j][e]) sum = v[j][e];
+        for (int i = tid; i < here; i += kThreads) {
+            const float l = to_f32(from[i]);
+            sum += some ? __builtin_amdgcn_exp2f((l - m) * kLog2e) : (l != l ? l : 0.f);
+        }
     }
     sum = wave_sum(sum);
     if (lane == 0) s_sum[wave] = sum;
@@ -178,21 +181,24 @@ __global__ __launch_bounds__(kThreads, 8) void beam_piece_kernel(const DT *logit
     const float bound = unordered(ob);
     const bool picky = some && ob > ordered(-__builtin_inff());
     const bool few = here <= kList;  // all of them fit the list
-    if (picky ? top >= bound : few) {
+    if (picky && top >= bound) {
 #pragma unroll
         for (int j = 0; j < VECS; ++j) {
-            if (picky && !(vtop[j] >= bound)) continue;
+            if (!(vtop[j] >= bound)) continue;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int at = (j * kThreads + tid) * 8 + e;
-                // places past the end are -inf, below any bound but this one
-                if (picky ? v[j][e] >= bound : at < here && v[j][e] == v[j][e]) {
+            for (int e = 0; e < 8; ++e)
+                if (v[j][e] >= bound) {  // places past the end are -inf
                     const int i = atomicAdd(&s_count, 1);
-                    if (i < kList) s_list[i] = key_of(v[j][e], first + at);
+                    if (i < kList)
+                        s_list[i] = key_of(v[j][e], first + (j * kThreads + tid) * 8 + e);
                 }
-            }
         }
     }
+    if (!picky && few)
+        for (int i = tid; i < here; i += kThreads) {
+            const float l = to_f32(from[i]);
+            if (l == l) s_list[atomicAdd(&s_count, 1)] = key_of(l, first + i);
+        }
     __syncthreads();
     if (tid == 0) {
         float all = s_sum[0];
