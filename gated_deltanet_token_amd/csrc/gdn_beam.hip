@@ -245,8 +245,9 @@ __global__ __launch_bounds__(kThreads, 8) void beam_piece_kernel(const DT *logit
 
 struct Cand {
     double score;
-    int64_t place;  // w V + v; -1: none
+    int64_t place;  // w 2^32 + v, in the order of w V + v; -1: none
 };
+__device__ __forceinline__ int64_t place_of(int w, int64_t v) { return (int64_t)w << 32 | v; }
 __device__ __forceinline__ bool before(const Cand &a, const Cand &b) {
     if (b.place < 0) return a.place >= 0;
     if (a.place < 0) return false;
@@ -278,15 +279,15 @@ __device__ __forceinline__ Cand candidate(const BeamRow &r, int w, int q, int W,
                                           int32_t eos, uint64_t key) {
     Cand d{-__builtin_inf(), -1};
     if (!r.live) {  // its tokens in order at -inf
-        if (q < W && q < V) d.place = w * V + q;
+        if (q < W && q < V) d.place = place_of(w, q);
     } else if (r.done) {  // itself, then its other tokens in order at -inf
         const int64_t v = q == 0 ? eos : (q - 1 < eos ? q - 1 : q);
         if (q == 0) d.score = r.score;
-        if (q < W && v < V) d.place = w * V + v;
+        if (q < W && v < V) d.place = place_of(w, v);
     } else if (key >> 32) {
         const float l = unordered((uint32_t)(key >> 32));
         d.score = (double)r.score + (((double)l - (double)r.m) - r.logsum);
-        d.place = w * V + (uint32_t)~(uint32_t)key;
+        d.place = place_of(w, (uint32_t)~(uint32_t)key);
     }
     return d;
 }
@@ -308,6 +309,7 @@ __global__ __launch_bounds__(THREADS) void beam_join_kernel(BeamParams p, int np
                                                             const uint64_t *best) {
     constexpr int kWaves = THREADS / 64;
     __shared__ BeamRow s_row[kMaxW];
+    __shared__ int32_t s_slot[kMaxW];
     __shared__ Cand s_list[kList];
     __shared__ uint32_t s_bound[kWaves];
     __shared__ int s_count;
@@ -327,24 +329,29 @@ __global__ __launch_bounds__(THREADS) void beam_join_kernel(BeamParams p, int np
     for (int w = wave; w < W; w += kWaves) {
         const int64_t row = (int64_t)b * W + w;
         const PieceSum *ps = sums + row * npieces;
-        float m = -__builtin_inff();
-        bool nan = false;
-        for (int i = lane; i < npieces; i += 64) {
+        const float s = p.scores[row];
+        const bool done = p.finished && p.finished[row];
+        if (p.src_slots && lane == 0) s_slot[w] = p.slots[row];
+        PieceSum own{-__builtin_inff(), 0.f};  // the lane's first piece, and often its only one
+        if (lane < npieces) own = ps[lane];
+        float m = own.m;
+        bool nan = own.m != own.m;
+        for (int i = lane + 64; i < npieces; i += 64) {
             nan |= ps[i].m != ps[i].m;
             m = fmaxf(m, ps[i].m);
         }
         m = wave_max(m);
         nan = __ballot(nan) != 0;
         double sum = 0.0;
-        if (m > -__builtin_inff())
-            for (int i = lane; i < npieces; i += 64)
+        if (m > -__builtin_inff()) {
+            if (own.m > -__builtin_inff()) sum = (double)own.sum * exp((double)own.m - (double)m);
+            for (int i = lane + 64; i < npieces; i += 64)
                 if (ps[i].m > -__builtin_inff())
                     sum += (double)ps[i].sum * exp((double)ps[i].m - (double)m);
+        }
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o);
         if (lane == 0) {
-            const float s = p.scores[row];
-            const bool done = p.finished && p.finished[row];
             const bool live = fabsf(s) < __builtin_inff() &&
                               (done || (!nan && m > -__builtin_inff()));
             s_row[w] = BeamRow{live && !done ? log(sum) : 0.0, m, s, done, live};
@@ -353,14 +360,14 @@ __global__ __launch_bounds__(THREADS) void beam_join_kernel(BeamParams p, int np
     __syncthreads();
 
     const auto write = [&](int k, const Cand &c) {
-        const int w = (int)(c.place / V);
-        const int32_t v = (int32_t)(c.place - w * V);
+        const int w = (int)(c.place >> 32);
+        const int32_t v = (int32_t)c.place;
         const int64_t to = (int64_t)b * W + k;
         p.new_scores[to] = (float)c.score;
         p.tokens[to] = v;
         p.parents[to] = w;
         if (p.new_finished) p.new_finished[to] = s_row[w].done || v == p.eos;
-        if (p.src_slots) p.src_slots[to] = p.slots[(int64_t)b * W + w];
+        if (p.src_slots) p.src_slots[to] = s_slot[w];
     };
 
     if (held) {
