@@ -167,7 +167,7 @@ size_t gdn_scan_workspace_size(int32_t num_seqs, int64_t tokens, int32_t D, gdn_
     if (packed && tokens > 0x7FFFFFFF) return 0;
     int64_t total = packed ? tokens : num_seqs;
     if (!packed && !mul_ok(total, tokens)) return 0;
-    if (bytes_of(total, D, 4) < 0) return 0;
+    if (D > kMaxScanWidth || bytes_of(total, D, 4) < 0 || !scan_fits(total, num_seqs, D)) return 0;
     int cus = 0;
     if (gdn::device_cus(&cus) != GDN_OK) return 0;
     return gdn::scan_workspace_bytes(num_seqs, tokens, D, code(dtype), packed != 0, cus);

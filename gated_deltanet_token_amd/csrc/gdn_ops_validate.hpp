@@ -56,6 +56,12 @@ struct ScanArgs {
     size_t ws_bytes;
 };
 
+// Workgroups of a scan call: a tile of tokens by at least 64 channels each.
+static inline bool scan_fits(int64_t tokens, int64_t nstates, int32_t D) {
+    int64_t wgs = tokens / GDN_SCAN_TILE + nstates;
+    return mul_ok(wgs, (D + (int64_t)63) / 64 + 8) && wgs <= kMaxGrid;
+}
+
 static inline gdn_status_t check_scan_common(const ScanArgs &s, int64_t &nx, int64_t &nst,
                                              int64_t &npre) {
     if (s.nstates < 1 || s.tokens < 0 || s.D < 1) return GDN_ERR_BAD_SHAPE;
@@ -66,10 +72,7 @@ static inline gdn_status_t check_scan_common(const ScanArgs &s, int64_t &nx, int
     nst = bytes_of(s.nstates, s.D, 4);
     npre = s.prefix ? bytes_of(s.prefix_rows, s.D, 4) : 0;
     if (nx < 0 || nst < 0 || npre < 0) return GDN_ERR_BAD_SHAPE;
-    // workgroups: a tile of tokens (or a piece of one) by at least 64 channels
-    const int64_t cb = (s.D + 63) / 64;
-    int64_t wgs = s.tokens / GDN_SCAN_TILE + s.nstates;
-    if (!mul_ok(wgs, cb + 8) || wgs > kMaxGrid) return GDN_ERR_BAD_SHAPE;
+    if (!scan_fits(s.tokens, s.nstates, s.D)) return GDN_ERR_BAD_SHAPE;
     if (s.tokens > 0 && (!s.x || !s.a)) return GDN_ERR_NULL_POINTER;
     if (s.cu_count > 0 && !s.cu) return GDN_ERR_NULL_POINTER;
     if (s.ws_bytes > (size_t)INT64_MAX) return GDN_ERR_BAD_SHAPE;
