@@ -13,6 +13,11 @@ The recurrence, per sequence and value head h (q/k head h // (Hv // Hk)):
 States are fp32 [.., Hv, Dv, Dk] (S in R^{Dv x Dk}, row-major).
 `flags` (GDN_QK_L2NORM | GDN_GATE_LOGITS) moves the input preparation into
 the kernels: raw q/k rows are L2-normalised, alpha/beta are given as logits.
+
+Beside the mixer: the gated linear recurrence with its gradients (gdn_scan_*),
+RMS norm with the residual's addition and an 8-bit output (gdn_rms_norm*),
+and beam search's selection over state slots (gdn_beam_select,
+gdn_gather_states).
 """
 from __future__ import annotations
 
