@@ -247,7 +247,7 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads), 4) void scan_backwa
         }
         // alpha and beta as fp32 for both sweeps, where they fit the registers of
         // two workgroups per CU; else they are formed twice
-        constexpr bool HOLD = sizeof(DT) == 2 && R * VEC <= 16;
+        constexpr bool HOLD = SPLIT > 0 && sizeof(DT) == 2 && R * VEC <= 16;
         float al[HOLD ? R : 1][VEC], be[HOLD ? R : 1][VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
@@ -371,7 +371,9 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads), 4) void scan_backwa
         }
     };
     do {
-        if (len - t0 >= Sh::kRows)
+        // code apart for whole tiles where the registers allow it (-1 %)
+        constexpr bool APART = SPLIT > 0 && sizeof(DT) == 2;
+        if (APART && len - t0 >= Sh::kRows)
             run_tile(std::true_type(), Sh::kRows);
         else
             run_tile(std::false_type(), (int)(len - t0 < Sh::kRows ? len - t0 : Sh::kRows));
