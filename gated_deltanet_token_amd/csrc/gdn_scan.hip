@@ -70,7 +70,7 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_forward_k
     constexpr int G = Sh::kGroups, C = Sh::kCols, R = Sh::kPer;
     __shared__ float s_a[G][C], s_h[G][C];
 
-    __shared__ int s_take[2];
+    __shared__ int s_take[3];
     const int pair = SPLIT > 0 ? 0 : sp.runs.chain(blockIdx.x);
     ScanTile mine{pair / ncb, pair % ncb, 0, 0};
     if constexpr (SPLIT > 0) mine = take_tile<false>(p, sp, ncb, s_take);
@@ -196,7 +196,7 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads), 4) void scan_backwa
     constexpr int G = Sh::kGroups, C = Sh::kCols, R = Sh::kPer;
     __shared__ float s_a[G][C], s_h[G][C], s_k[G][C];
 
-    __shared__ int s_take[2];
+    __shared__ int s_take[3];
     const int pair = SPLIT > 0 ? 0 : sp.runs.chain(blockIdx.x);
     ScanTile mine{pair / ncb, pair % ncb, 0, 0};
     if constexpr (SPLIT > 0) mine = take_tile<true>(p, sp, ncb, s_take);
@@ -478,12 +478,16 @@ ScanLayout scan_layout(int64_t nseq, int64_t tokens, int32_t D, int cols, bool p
     return l;
 }
 
-// Whether a call is cut along time: sequences of more than one tile, and not
-// enough (sequence, column block) pairs to fill the device with one workgroup
-// each.
+// Whether a call is cut along time: sequences of more than one tile, and either
+// not enough (sequence, column block) pairs to fill the device with one
+// workgroup each (128 x 512 x 2,048 bf16, 16 pairs per CU: 194 us uncut, 197
+// cut; 33 packed sequences of 20,011 x 2,048 fp32, 4 pairs: 227 and 136), or a
+// packed batch of a tile per sequence or more on average, whose longest
+// sequence may be most of it (128 sequences, 24,576 x 4,096: 221 uncut, 215 cut;
+// shorter ones lose, 300 sequences, 24,576 x 2,048: 138 and 172).
 bool scan_wants_split(int64_t nseq, int64_t tokens, int64_t ncb, bool packed, int cus) {
-    (void)packed;
-    return tokens > GDN_SCAN_TILE && nseq * ncb < 8 * (int64_t)cus;
+    if (tokens <= GDN_SCAN_TILE) return false;
+    return nseq * ncb < 8 * (int64_t)cus || (packed && tokens >= nseq * GDN_SCAN_TILE);
 }
 
 constexpr int kForVec = 8;

@@ -305,15 +305,26 @@ __device__ __forceinline__ int64_t scan_first_slot(const ScanParams &p, int n) {
 }
 
 // The sequence of a slot: the last one that starts at or before it, looked for
-// by the whole workgroup at once (a binary search would be a chain of loads in
-// front of every tile). s_seq starts at 0, and every thread reaches this call.
-__device__ __forceinline__ int scan_slot_sequence(const ScanParams &p, int64_t slot, int *s_seq) {
-    int last = 0;
-    for (int n = threadIdx.x; n < p.N; n += blockDim.x)
-        if (scan_first_slot(p, n) <= slot) last = n;
-    if (last > 0) atomicMax(s_seq, last);
-    __syncthreads();
-    return __builtin_amdgcn_readfirstlane(*s_seq);
+// by the whole workgroup, which probes as many sequences at once as it has
+// threads (a binary search by one thread would be a chain of loads in front of
+// every tile). s_found[0] starts at 0, and every thread reaches this call.
+__device__ __forceinline__ int scan_slot_sequence(const ScanParams &p, int64_t slot,
+                                                  int *s_found) {
+    int lo = 0, size = p.N, turn = 0;
+    while (size > 1) {
+        const int step = (size + (int)blockDim.x - 1) / (int)blockDim.x;
+        const int at = (int)threadIdx.x * step;
+        if (threadIdx.x == 0) s_found[turn ^ 1] = 0;  // of the round after this one
+        if (at > 0 && at < size && scan_first_slot(p, lo + at) <= slot)
+            atomicMax(s_found + turn, at);
+        __syncthreads();
+        const int found = __builtin_amdgcn_readfirstlane(s_found[turn]);
+        lo += found;
+        size = min(step, size - found);
+        turn ^= 1;
+        __syncthreads();
+    }
+    return lo;
 }
 
 }  // namespace gdn

@@ -438,3 +438,26 @@ def test_debug_checks_offsets(gdn, monkeypatch):
                                          prefix_interval=2)
     c = torch.tensor([0, 100, 300], dtype=torch.int32, device=DEV)
     gdn.gdn_scan_varlen_prefill(x, x, x, c)
+
+
+@gpu
+@pytest.mark.parametrize("N,most,D", [(700, 3, 8), (5000, 40, 8), (1100, 400, 16)])
+def test_many_packed_sequences(gdn, N, most, D):
+    """More sequences than a workgroup has threads: the same bits with and without a workspace, and
+    each final state from the oracle on its own tokens."""
+    g = torch.Generator().manual_seed(N)
+    lengths = torch.randint(0, most, (N,), generator=g)
+    lengths[N // 2] = 1000
+    cu = torch.cat([torch.zeros(1), lengths.cumsum(0)]).to(torch.int32)
+    total = int(cu[-1])
+    x, a, b, s = inputs(N, total, D, N, torch.float32, False, True)
+    xd, ad, bd, sd, cud = dev(x, a, b, s, cu)
+    out, fin = gdn.gdn_scan_varlen_prefill(xd, ad, bd, cud, sd, flags=2)
+    out2, fin2 = gdn.gdn_scan_varlen_prefill(xd, ad, bd, cud, sd, flags=2, workspace=None)
+    assert torch.equal(out, out2) and torch.equal(fin, fin2)
+    for n in [0, 1, N // 3, N // 2 - 1, N // 2, N // 2 + 1, N - 2, N - 1]:
+        lo, hi = int(cu[n]), int(cu[n + 1])
+        h, e = scan64(x[lo:hi], a[lo:hi], b[lo:hi], s[n], True)
+        assert_scan_close(out[lo:hi], h, e, torch.float32, n)
+        assert_scan_close(fin[n], h[-1] if hi > lo else s[n].double(),
+                          e[-1] if hi > lo else torch.zeros(D).double(), torch.float32, n)
