@@ -212,3 +212,23 @@ def test_many_candidates(gdn, W, V):
     g = torch.Generator(device=DEV).manual_seed(V)
     x = (torch.randn(1, W, V, generator=g, device=DEV) * 3).bfloat16().cpu()
     check(gdn, x, torch.randn(1, W, generator=torch.Generator().manual_seed(W)))
+
+
+@gpu
+def test_offsets_past_32_bits(gdn):
+    """Logits of over 2^31 elements and states of over 2^32 bytes: the last item is that of a call
+    on it alone."""
+    B, W, V = 66, 32, 1_050_000
+    x = torch.randn(B, W, V, generator=torch.Generator(device=DEV).manual_seed(9), device=DEV,
+                    dtype=torch.bfloat16)
+    s = torch.randn(B, W, generator=torch.Generator().manual_seed(9)).to(DEV)
+    out = gdn.gdn_beam_select(x, s)
+    one = gdn.gdn_beam_select(x[-1:].clone(), s[-1:].clone())
+    for p, q in zip(out[:3], one):
+        assert torch.equal(p[-1:], q)
+    del x
+    states = torch.arange(1500, dtype=torch.float32, device=DEV)[:, None].expand(
+        1500, 786432).contiguous()
+    idx = torch.randperm(1500, generator=torch.Generator().manual_seed(2)).to(torch.int32).to(DEV)
+    moved = gdn.gdn_gather_states(states, idx)
+    assert torch.equal(moved[:, 0], idx.float()) and torch.equal(moved[:, -1], idx.float())

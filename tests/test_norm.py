@@ -198,3 +198,20 @@ def test_backward_against_differences(gdn):
     noise = 4 * REL * (exact(1).abs() * dy.double().abs()).sum() / (2 * step)
     assert abs(diff - lin) <= curve + noise
     assert curve <= 0.05 * abs(lin) + 1.0
+
+
+@gpu
+def test_offsets_past_32_bits(gdn):
+    """Over 2^32 bytes and 2^31 elements: the last rows are those of a call on them alone."""
+    rows, D = 550_001, 4096
+    g = torch.Generator(device=DEV).manual_seed(5)
+    x = torch.randn(rows, D, generator=g, device=DEV, dtype=torch.bfloat16)
+    w = torch.randn(D, generator=g, device=DEV, dtype=torch.bfloat16)
+    out, q, s, r = gdn.gdn_rms_norm(x, w, x, group=128, want_out8=True)
+    n = 7
+    o1, q1, s1, r1 = gdn.gdn_rms_norm(x[-n:].clone(), w, x[-n:].clone(), group=128, want_out8=True)
+    assert torch.equal(out[-n:], o1) and torch.equal(r[-n:], r1) and torch.equal(s[-n:], s1)
+    assert torch.equal(q[-n:].view(torch.uint8), q1.view(torch.uint8))
+    dx, dw = gdn.gdn_rms_norm_backward(out, x, w)
+    d1, _ = gdn.gdn_rms_norm_backward(out[-n:].clone(), x[-n:].clone(), w)
+    assert torch.equal(dx[-n:], d1) and dw.isfinite().all()

@@ -461,3 +461,33 @@ def test_many_packed_sequences(gdn, N, most, D):
         assert_scan_close(out[lo:hi], h, e, torch.float32, n)
         assert_scan_close(fin[n], h[-1] if hi > lo else s[n].double(),
                           e[-1] if hi > lo else torch.zeros(D).double(), torch.float32, n)
+
+
+@gpu
+def test_backward_past_32_bits(gdn):
+    """Gradients of tensors over 2^32 bytes: the last tokens' are those of a call on them alone
+    from the prefix state in front of them, bit by bit."""
+    T, D = 360_065, 6144
+    make = lambda seed, shift=0.0: torch.randn(  # noqa: E731
+        1, T, D, generator=torch.Generator(device=DEV).manual_seed(seed), device=DEV,
+        dtype=torch.bfloat16) + shift
+    x, a, b, dy = make(1), make(2, -3.0), make(3), make(4)
+    pre = torch.empty(T // 128, D, device=DEV)
+    kw = dict(flags=2, prefix_interval=2)
+    out, _ = gdn.gdn_scan_prefill(x, a, b, prefix_states=pre, **kw)
+    del out
+    grads = gdn.gdn_scan_backward(dy, x, a, b, prefix_states=pre, **kw)
+    lo = (T // 128 - 3) * 128
+    cut = lambda t: t[:, lo:].contiguous()  # noqa: E731
+    tail = gdn.gdn_scan_backward(cut(dy), cut(x), cut(a), cut(b), pre[lo // 128 - 1][None].clone(),
+                                 prefix_states=pre[lo // 128:].clone(), **kw)
+    for p, q in zip(grads[:3], tail):
+        assert torch.equal(p[:, lo:], q)
+    # the tokens in front of them: what reaches them is the tail's gradient of its first state
+    mid = lo - 256
+    part = lambda t: t[:, mid:lo].contiguous()  # noqa: E731
+    front = gdn.gdn_scan_backward(part(dy), part(x), part(a), part(b),
+                                  pre[mid // 128 - 1][None].clone(), dfinal=tail[3],
+                                  prefix_states=pre[mid // 128:lo // 128].clone(), **kw)
+    for p, q in zip(grads[:3], front):
+        assert torch.equal(p[:, mid:lo], q)
