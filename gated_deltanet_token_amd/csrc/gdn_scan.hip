@@ -38,15 +38,15 @@ __device__ __forceinline__ ScanTile take_tile(const ScanParams &p, const ScanSpl
     }
     __syncthreads();
     int64_t k = __builtin_amdgcn_readfirstlane(s_take[0]);  // uniform, and known to be
+    if (k < 0 || k >= sp.per_chain) return ScanTile{-1, 0, 0, 0};
+    if (BACK) k = sp.per_chain - 1 - k;
     ScanTile t;
     if (p.cu) {
-        if (BACK) k = sp.slots - 1 - k;
         t.cb = chain;
         t.slot = k;
         t.n = scan_slot_sequence(p, k, s_take + 1);
         t.tile = k - scan_first_slot(p, t.n);
     } else {
-        if (BACK) k = sp.slots / p.N - 1 - k;
         t.n = chain / ncb;
         t.cb = chain - t.n * ncb;
         t.tile = k;

@@ -220,7 +220,10 @@ __device__ __forceinline__ int64_t scan_block_ending(const ScanParams &p, int64_
 // Workgroups take the tiles of a chain in order from a counter. A tile waits
 // only for tiles of its chain that were taken before it, by workgroups that run
 // already and in turn wait only for earlier ones, and every taken tile
-// publishes: every wait ends.
+// publishes: every wait ends. A wait is bounded all the same (about 3 s, where
+// a right one takes microseconds) and a count from the counter is checked: a
+// caller that lets two calls overlap on one workspace gets NaN or tiles left
+// out, and neither a hang nor an access out of range.
 struct ScanSplit {
     uint32_t *ticket;  // [chains]
     uint64_t *map;     // [slots][width], SPLIT > 1: A low, H high
@@ -233,6 +236,7 @@ struct ScanSplit {
 };
 
 constexpr uint32_t kAbsent = 0xFFFFFFFFu;
+constexpr int kScanSpins = 1 << 22;  // looks of about 0.7 us
 
 // A value's bits; any NaN becomes the plain one, never kAbsent.
 __device__ __forceinline__ uint32_t scan_word(float x) {
@@ -260,13 +264,13 @@ __device__ __forceinline__ float find_state(const ScanSplit &sp, int64_t at, int
                                             int32_t ahead, int col) {
     if constexpr (SPLIT == 1) {
         const uint32_t *p = sp.state + at * sp.width + col;
-        for (;;) {
+        for (int spin = 0; spin < kScanSpins; ++spin) {
             const uint32_t w = observe(p);
             if (w != kAbsent) return __builtin_bit_cast(float, w);
             __builtin_amdgcn_s_sleep(1);
         }
     } else {
-        for (;;) {
+        for (int spin = 0; spin < kScanSpins; ++spin) {
             uint32_t state[SPLIT];
             uint64_t map[SPLIT];
 #pragma unroll
@@ -293,6 +297,7 @@ __device__ __forceinline__ float find_state(const ScanSplit &sp, int64_t at, int
             __builtin_amdgcn_s_sleep(1);
         }
     }
+    return __builtin_nanf("");
 }
 
 // First slot of sequence n of a packed batch: it owns the slots from

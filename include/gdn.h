@@ -416,7 +416,7 @@ gdn_status_t gdn_scan_decode(const void *x, const void *alpha, const void *beta,
  * gdn_scan_workspace_size -- bytes of workspace the scan calls can use:
  * packed = 0: num_seqs = B, tokens = T; packed = 1: num_seqs = N,
  * tokens = total_T. 0 when the call would not use one (sequences of one tile,
- * or enough of them to fill the device), when an argument is invalid, or when
+ * or enough equal ones to fill the device), when an argument is invalid, or when
  * no device is available.
  */
 size_t gdn_scan_workspace_size(int32_t num_seqs, int64_t tokens, int32_t D, gdn_dtype_t dtype,
