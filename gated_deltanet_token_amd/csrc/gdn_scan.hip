@@ -59,7 +59,7 @@ __device__ __forceinline__ ScanTile take_tile(const ScanParams &p, const ScanSpl
 // (sequence, column block), its tiles in order: enough where that alone fills
 // the device, and without a workspace.
 //
-// Bound by HBM: 65,536 x 6,144 bf16 601 us (5.4 TB/s, the reads and writes
+// Bound by HBM: 65,536 x 6,144 bf16 608 us (5.3 TB/s, the reads and writes
 // counted at 1.01 times the tensors), 20,011 x 2,048 fp32 packed 130 us. Two
 // workgroups per CU (4 waves per SIMD) hold 196 KiB of loads in flight; gates
 // are formed once and kept with the products beta x as fp32.
@@ -185,7 +185,7 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_forward_k
 // the decay's gradient does not inherit a rounding of one.
 //
 // 7 elements of traffic per token and channel against some 60 vector
-// instructions, each of them counted: 4 x 4,097 x 2,048 bf16 98 us, 4.8 TB/s.
+// instructions, each of them counted: 4 x 4,097 x 2,048 bf16 100 us, 4.7 TB/s.
 // Registers decide: at most 128, for two workgroups per CU, so a thread holds 4
 // columns of bf16 (not 8: 143 us against 117 when that was chosen), the raw
 // words rather than their values, and one pair of columns' gradients at a time.
@@ -443,7 +443,7 @@ template <typename DT, int VEC> int column_blocks(int32_t D) {
 
 // Sets a SPLIT launch's workspace: counters to 0, words to absent. A kernel and
 // not a memset, whose node in a replayed graph is not to be relied on. 12.6 MB
-// for 65,536 x 6,144: 6 us beside 601.
+// for 65,536 x 6,144: 6 us beside 608.
 __global__ __launch_bounds__(256) void scan_clear_kernel(u32x4 *ws, int64_t zero, int64_t total) {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
          i += (int64_t)gridDim.x * 256) {
