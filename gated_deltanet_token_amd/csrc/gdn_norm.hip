@@ -272,9 +272,10 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p) {
 
 // dx per row, and each workgroup's share of dw: a thread keeps the sums of its
 // columns over the workgroup's rows, the workgroup joins the threads that hold
-// the same columns, and norm_dweight_kernel joins the workgroups in order. 512
-// workgroups, two per CU: more would only lengthen that join. 8,191 x 4,096 bf16
-// 47 us (5.7 TB/s).
+// the same columns, and norm_dweight_kernel joins the workgroups in order. As
+// many workgroups as give every CU 1,024 threads, but at least 512, and at least
+// 4 rows for each of them (forward and backward of 16,384 x 1,024 bf16 58 us, 82
+// with 512; 12,741 x 531 49 and 85). 8,191 x 4,096 bf16 47 us (5.7 TB/s).
 template <typename DT, bool VEC, int TPR, int CH>
 __global__ __launch_bounds__(1024) void norm_backward_kernel(NormBackwardParams p) {
     __shared__ float s_red[2][16];
@@ -359,12 +360,12 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormBackwardParams 
         }
     }
     if (!p.dw) return;
-    float *part = p.partial + (int64_t)blockIdx.x * D;
+    float *part = p.partial + (int64_t)blockIdx.x * norm_partial_width(D);
     if constexpr (TPR == 0) {
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
             const int c = (k * tpr + j) * 8;
-            if (c < D) store8<float, VEC, false>(part + c, D - c, dw[k]);
+            if (c < D) store8<float, true, false>(part + c, 8, dw[k]);
         }
     } else {
 #pragma unroll
@@ -382,20 +383,20 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormBackwardParams 
 #pragma unroll
             for (int k = 0; k < CH; ++k) {
                 const int c = (k * tpr + j) * 8;
-                if (c < D) store8<float, VEC, false>(part + c, D - c, dw[k]);
+                if (c < D) store8<float, true, false>(part + c, 8, dw[k]);
             }
         }
     }
 }
 
 // dw[c] = sum over the partials in a fixed order: 32 columns per workgroup, 4
-// per lane where a partial row starts on 16 bytes, 128 threads (or 32) beside
-// each other down the partials. 512 x 4,096 in 4.0 us (one lane per column and 16
+// per lane (partial rows are padded to 8 columns), 128 threads beside each other
+// down the partials. 512 x 4,096 in 4.0 us (one lane per column and 16
 // threads down took 9.5: too few loads at once).
-template <int VEC>
 __global__ __launch_bounds__(1024) void norm_dweight_kernel(const float *partial, int count,
                                                             float *dw, int D) {
-    constexpr int kLanes = 32 / VEC, kParts = 1024 / kLanes;
+    constexpr int VEC = 4, kLanes = 32 / VEC, kParts = 1024 / kLanes;
+    const int width = norm_partial_width(D);
     __shared__ float s_sum[16][32];
     const int l = threadIdx.x % kLanes, part = threadIdx.x / kLanes;
     const int c = blockIdx.x * 32 + l * VEC;
@@ -405,14 +406,9 @@ __global__ __launch_bounds__(1024) void norm_dweight_kernel(const float *partial
     if (c < D)
 #pragma unroll 4
         for (int i = part; i < count; i += kParts) {
-            const float *from = partial + (int64_t)i * D + c;
-            if constexpr (VEC == 4) {
-                const f32x4 x = *reinterpret_cast<const f32x4 *>(from);
+            const f32x4 x = *reinterpret_cast<const f32x4 *>(partial + (int64_t)i * width + c);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sum[e] += x[e];
-            } else {
-                sum[0] += from[0];
-            }
+            for (int e = 0; e < VEC; ++e) sum[e] += x[e];
         }
     // the parts of a wave, then the 16 waves
 #pragma unroll
@@ -501,10 +497,12 @@ hipError_t launch_norm(const NormParams &p, int dtype, hipStream_t stream) {
     return with_norm_types(dtype, p.D, plan_norm(p.D), RunNorm{p, stream});
 }
 
-// Workgroups of the backward pass, each with a row of partial sums.
+// Workgroups of the backward pass (see its kernel), each with a row of partial sums.
 int norm_partials(int64_t rows, int32_t D) {
-    const int64_t per = plan_norm(D).per, wgs = (rows + per - 1) / per;
-    return (int)(wgs < 512 ? wgs : 512);
+    const NormPlan n = plan_norm(D);
+    const int64_t wgs = (rows + n.per - 1) / n.per, fill = (1 << 18) / n.threads;
+    const int64_t most = std::max<int64_t>(512, std::min(fill, wgs / 4));
+    return (int)std::min(wgs, most);
 }
 
 hipError_t launch_norm_backward(const NormBackwardParams &p, int dtype, hipStream_t stream) {
@@ -516,12 +514,8 @@ hipError_t launch_norm_backward(const NormBackwardParams &p, int dtype, hipStrea
     }
     if (p.dw) {
         const dim3 grid((unsigned)((p.D + 31) / 32)), block(1024);
-        if (p.D % 4 == 0)
-            hipLaunchKernelGGL(norm_dweight_kernel<4>, grid, block, 0, stream, p.partial, count,
-                               p.dw, p.D);
-        else
-            hipLaunchKernelGGL(norm_dweight_kernel<1>, grid, block, 0, stream, p.partial, count,
-                               p.dw, p.D);
+        hipLaunchKernelGGL(norm_dweight_kernel, grid, block, 0, stream, p.partial, count, p.dw,
+                           p.D);
     }
     return hipGetLastError();
 }

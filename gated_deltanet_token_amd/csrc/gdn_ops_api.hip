@@ -188,7 +188,7 @@ gdn_status_t gdn_rms_norm(const void *x, const void *residual, const void *weigh
 
 size_t gdn_rms_norm_workspace_size(int64_t rows, int32_t D) {
     if (rows < 1 || rows > kMaxGrid || D < 1 || D > kMaxNormWidth) return 0;
-    return (size_t)gdn::norm_partials(rows, D) * D * 4;
+    return (size_t)gdn::norm_partials(rows, D) * gdn::norm_partial_width(D) * 4;
 }
 
 gdn_status_t gdn_rms_norm_backward(const void *dout, const void *r, const void *weight,

@@ -69,7 +69,7 @@ struct NormBackwardParams {
     const void *dout, *r, *w, *dres;
     void *dx;
     float *dw;
-    float *partial;  // [norm_partials(rows, D)][D]
+    float *partial;  // [norm_partials(rows, D)][norm_partial_width(D)]
     int64_t rows;
     int32_t D;
     float eps, inv_d;  // inv_d: 1 / D
@@ -77,6 +77,7 @@ struct NormBackwardParams {
 
 hipError_t launch_norm(const NormParams &p, int dtype, hipStream_t stream);
 int norm_partials(int64_t rows, int32_t D);
+constexpr int norm_partial_width(int D) { return (D + 7) / 8 * 8; }
 hipError_t launch_norm_backward(const NormBackwardParams &p, int dtype, hipStream_t stream);
 
 struct BeamParams {
