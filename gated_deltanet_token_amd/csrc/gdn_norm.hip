@@ -273,9 +273,10 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p) {
 // dx per row, and each workgroup's share of dw: a thread keeps the sums of its
 // columns over the workgroup's rows, the workgroup joins the threads that hold
 // the same columns, and norm_dweight_kernel joins the workgroups in order. As
-// many workgroups as give every CU 1,024 threads, but at least 512, and at least
-// 4 rows for each of them (forward and backward of 16,384 x 1,024 bf16 58 us, 82
-// with 512; 12,741 x 531 49 and 85). 8,191 x 4,096 bf16 47 us (5.7 TB/s).
+// many workgroups as give every CU 1,024 threads, but not under 512 unless the
+// rows are fewer, and 4 turns for each above that (16,384 x 2,048 bf16, both
+// directions, 98 us, 112 with 512, 103 with 2,048 threads). 8,191 x 4,096 bf16
+// 47 us (5.7 TB/s).
 template <typename DT, bool VEC, int TPR, int CH>
 __global__ __launch_bounds__(1024) void norm_backward_kernel(NormBackwardParams p) {
     __shared__ float s_red[2][16];
@@ -434,21 +435,28 @@ struct NormPlan {
     int tpr, ch, threads, per;
 };
 
-NormPlan plan_norm(int32_t D) {
+// The backward pass stays with one wave up to 1,024 columns, without a barrier
+// (16,384 x 1,024 bf16, both directions, 52 against 59 us); the forward one does
+// not, whose workgroups read rows once past the caches (32,768 x 1,024 41
+// against 44 us).
+NormPlan plan_norm(int32_t D, bool back) {
     const int chunks = (D + 7) / 8;
     if (chunks <= 16) return {16, 1, 256, 16};
     if (chunks <= 64) return {64, 1, 256, 4};
+    if (back && chunks <= 128) return {64, 2, 256, 4};
     const int ch = chunks > 1024 ? 2 : 1;
     const int threads = ((chunks + ch - 1) / ch + 63) / 64 * 64;
     return {0, ch, threads, 1};
 }
 
-template <typename F> hipError_t with_norm_types(int dtype, int32_t D, const NormPlan &n, F &&f) {
+template <typename F> hipError_t with_norm_types(int dtype, int32_t D, const NormPlan &n, const F &f) {
     const bool vec = D % 8 == 0;
 #define GDN_NORM_CASE(DT, VEC)                                                   \
     do {                                                                         \
         if (n.tpr == 16) return f.template run<DT, VEC, 16, 1>(n);               \
-        if (n.tpr == 64) return f.template run<DT, VEC, 64, 1>(n);               \
+        if (n.tpr == 64 && n.ch == 1) return f.template run<DT, VEC, 64, 1>(n);  \
+        if constexpr (F::kBack)                                                  \
+            if (n.tpr == 64) return f.template run<DT, VEC, 64, 2>(n);           \
         if (n.ch == 1) return f.template run<DT, VEC, 0, 1>(n);                  \
         return f.template run<DT, VEC, 0, 2>(n);                                 \
     } while (0)
@@ -462,6 +470,7 @@ template <typename F> hipError_t with_norm_types(int dtype, int32_t D, const Nor
 }
 
 struct RunNorm {
+    static constexpr bool kBack = false;
     const NormParams &p;
     hipStream_t stream;
     template <typename DT, bool VEC, int TPR, int CH> hipError_t run(const NormPlan &n) const {
@@ -481,6 +490,7 @@ struct RunNorm {
 };
 
 struct RunNormBackward {
+    static constexpr bool kBack = true;
     const NormBackwardParams &p;
     hipStream_t stream;
     template <typename DT, bool VEC, int TPR, int CH> hipError_t run(const NormPlan &n) const {
@@ -494,12 +504,12 @@ struct RunNormBackward {
 }  // namespace
 
 hipError_t launch_norm(const NormParams &p, int dtype, hipStream_t stream) {
-    return with_norm_types(dtype, p.D, plan_norm(p.D), RunNorm{p, stream});
+    return with_norm_types(dtype, p.D, plan_norm(p.D, false), RunNorm{p, stream});
 }
 
 // Workgroups of the backward pass (see its kernel), each with a row of partial sums.
 int norm_partials(int64_t rows, int32_t D) {
-    const NormPlan n = plan_norm(D);
+    const NormPlan n = plan_norm(D, true);
     const int64_t wgs = (rows + n.per - 1) / n.per, fill = (1 << 18) / n.threads;
     const int64_t most = std::max<int64_t>(512, std::min(fill, wgs / 4));
     return (int)std::min(wgs, most);
@@ -509,7 +519,7 @@ hipError_t launch_norm_backward(const NormBackwardParams &p, int dtype, hipStrea
     const int count = norm_partials(p.rows, p.D);
     if (count > 0) {
         const hipError_t e =
-            with_norm_types(dtype, p.D, plan_norm(p.D), RunNormBackward{p, stream});
+            with_norm_types(dtype, p.D, plan_norm(p.D, true), RunNormBackward{p, stream});
         if (e != hipSuccess) return e;
     }
     if (p.dw) {

@@ -215,3 +215,12 @@ def test_offsets_past_32_bits(gdn):
     dx, dw = gdn.gdn_rms_norm_backward(out, x, w)
     d1, _ = gdn.gdn_rms_norm_backward(out[-n:].clone(), x[-n:].clone(), w)
     assert torch.equal(dx[-n:], d1) and dw.isfinite().all()
+
+
+@gpu
+@pytest.mark.parametrize("rows,D", [(9000, 531), (4100, 1024), (5003, 2048), (17000, 72),
+                                    (2100, 1016), (2049, 520)], ids=str)
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_backward_of_many_rows(gdn, rows, D, dt):
+    """Workgroups that take several rows each, and more than 512 of them."""
+    test_backward(gdn, rows, D, dt, True)
