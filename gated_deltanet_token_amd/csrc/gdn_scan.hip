@@ -432,6 +432,7 @@ hipError_t with_scan_types(int dtype, int32_t D, const void *b, uint32_t flags, 
     const bool tied = b == nullptr, logits = flags & GDN_GATE_LOGITS;
     if (dtype == 1)
         return D % BVEC == 0 ? with_scan_gates<__bf16, BVEC>(tied, logits, f)
+               : D % 2 == 0  ? with_scan_gates<__bf16, 2>(tied, logits, f)
                              : with_scan_gates<__bf16, 1>(tied, logits, f);
     return D % 4 == 0 ? with_scan_gates<float, 4>(tied, logits, f)
                       : with_scan_gates<float, 1>(tied, logits, f);
@@ -494,10 +495,11 @@ constexpr int kForVec = 8;
 constexpr int kBackVec = 4;  // columns per thread of the bf16 backward kernel
 
 int scan_cols(int32_t D, int dtype, bool back) {
-    if (dtype == 1 && back)
-        return D % kBackVec == 0 ? ScanShape<__bf16, kBackVec>::kCols : ScanShape<__bf16, 1>::kCols;
-    if (dtype == 1)
-        return D % kForVec == 0 ? ScanShape<__bf16, kForVec>::kCols : ScanShape<__bf16, 1>::kCols;
+    if (dtype == 1) {
+        if (back && D % kBackVec == 0) return ScanShape<__bf16, kBackVec>::kCols;
+        if (!back && D % kForVec == 0) return ScanShape<__bf16, kForVec>::kCols;
+        return D % 2 == 0 ? ScanShape<__bf16, 2>::kCols : ScanShape<__bf16, 1>::kCols;
+    }
     return D % 4 == 0 ? ScanShape<float, 4>::kCols : ScanShape<float, 1>::kCols;
 }
 

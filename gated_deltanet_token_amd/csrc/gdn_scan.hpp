@@ -160,11 +160,15 @@ __device__ __forceinline__ void gates(float a, float b, float &alpha, float &kee
 
 // A tile is kRows tokens by kCols channels on kThreads threads. kLanes
 // neighbouring lanes hold one token's kCols channels, VEC each; the kGroups
-// groups of them hold kPer consecutive tokens each.
+// groups of them hold kPer consecutive tokens each. Rows that start off 8 or 16
+// bytes are read in pairs of bf16 where the width is even: what such rows cost
+// is their segments that straddle cache lines, and a pair's are 256 bytes long
+// (5 x 2,143 x 7,764 186 us, 226 one by one in segments of 128 bytes, 229 in
+// fours of the same length; a width of 7,808 128).
 template <typename DT, int VEC> struct ScanShape {
-    static constexpr int kThreads = VEC == 1 ? 1024 : 512;
+    static constexpr int kThreads = VEC <= 2 ? 1024 : 512;
     static constexpr int kRows = GDN_SCAN_TILE;
-    static constexpr int kLanes = VEC == 1 ? 64 : 16;
+    static constexpr int kLanes = VEC <= 2 ? 64 : 16;
     static constexpr int kCols = kLanes * VEC;
     static constexpr int kGroups = kThreads / kLanes;
     static constexpr int kPer = kRows / kGroups;

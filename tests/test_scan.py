@@ -491,3 +491,30 @@ def test_backward_past_32_bits(gdn):
                                   prefix_states=pre[mid // 128:lo // 128].clone(), **kw)
     for p, q in zip(grads[:3], front):
         assert torch.equal(p[:, mid:lo], q)
+
+
+EVEN = [  # B, T, D, dtype, tied, logits, initial state: bf16 rows of pairs, not of 8 or 16 bytes
+    (1, 1, 2, "bf16", False, True, True), (2, 129, 126, "bf16", True, True, True),
+    (1, 260, 130, "bf16", False, False, False), (3, 385, 66, "bf16", True, False, True),
+    (2, 1000, 258, "bf16", False, True, True), (1, 300, 1102, "bf16", False, True, False),
+    (2, 257, 132, "bf16", False, True, True),
+]
+
+
+@gpu
+@pytest.mark.parametrize("case", EVEN, ids=str)
+def test_even_widths(gdn, case):
+    test_prompt(gdn, case)
+    test_backward(gdn, case, 1)
+    test_backward(gdn, case, 2)
+
+
+@gpu
+@pytest.mark.parametrize("tied", [False, True])
+def test_even_widths_elsewhere(gdn, tied):
+    """Packed, decoded and in many chains, as the other widths."""
+    # sequences that start on 16 bytes, which a call on one of them alone asks for
+    test_packed_is_each_sequence_alone(gdn, (0, 136, 8, 304, 0, 129), 134, "bf16", tied)
+    test_decode_slots(gdn, "bf16", 102, tied, 3)
+    test_many_chains(gdn, (3, 385, 2046, "bf16", tied))
+    test_many_chains(gdn, (2100, 130, 6, "bf16", tied))
