@@ -497,7 +497,7 @@ EVEN = [  # B, T, D, dtype, tied, logits, initial state: bf16 rows of pairs, not
     (1, 1, 2, "bf16", False, True, True), (2, 129, 126, "bf16", True, True, True),
     (1, 260, 130, "bf16", False, False, False), (3, 385, 66, "bf16", True, False, True),
     (2, 1000, 258, "bf16", False, True, True), (1, 300, 1102, "bf16", False, True, False),
-    (2, 257, 132, "bf16", False, True, True),
+    (2, 257, 132, "bf16", False, True, True), (2, 300, 160, "bf16", False, True, True),
 ]
 
 
