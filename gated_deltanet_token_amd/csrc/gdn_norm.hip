@@ -19,7 +19,7 @@ namespace gdn {
 
 namespace {
 
-constexpr float kE4m3Inv = 1.f / 448.f;  // of the largest e4m3 value
+constexpr float kE4m3Max = 448.f;
 constexpr float kScaleFloor = 0x1p-100f;  // groups of zeros keep a finite scale and its inverse
 
 // 1 / sqrt(x) to about a unit in its last place: the instruction's value and one
@@ -35,6 +35,28 @@ __device__ __forceinline__ float row16_max(float x) {
     x = fmaxf(x, GDN_DPP(x, 0x141));
     x = fmaxf(x, GDN_DPP(x, 0x140));
     return x;
+}
+
+// x / d for values that share a d > 0, as x times the inverse in two terms: off by
+// less than 2^-45 beside the one rounding, so that a quotient halfway between two
+// e4m3 values comes out exactly and goes to the even one (the rounded inverse
+// alone lands on either side). An infinite d gives 0, and NaN of an infinite x.
+struct Divide {
+    float high, low;
+    __device__ __forceinline__ explicit Divide(float d) {
+        const float r = __builtin_amdgcn_rcpf(d);
+        const float e = fmaf(-d, r, 1.f);  // 1 / d = r (1 + e + e^2 + ...), |e| < 2^-22
+        high = r;
+        low = d < __builtin_inff() ? r * fmaf(e, e, e) : 0.f;
+    }
+    __device__ __forceinline__ float operator()(float x) const { return fmaf(x, high, x * low); }
+};
+
+// The scale of a group whose largest magnitude is `most`: most / 448, rounded once.
+__device__ __forceinline__ float e4m3_scale(float most) {
+    constexpr float inv = 1.f / kE4m3Max;
+    const float q = most * inv;
+    return q < __builtin_inff() ? fmaxf(fmaf(fmaf(-q, kE4m3Max, most), inv, q), kScaleFloor) : q;
 }
 
 struct SumOp {
@@ -225,10 +247,10 @@ __device__ __forceinline__ void norm_row(const NormParams &p, int64_t row, int t
         if (p.group == 0) {
             most = fmaxf(most, m);
         } else {  // 128 columns: the 16 lanes of a DPP row
-            m = fmaxf(row16_max(m) * kE4m3Inv, kScaleFloor);
-            const float inv = __builtin_amdgcn_rcpf(m);
+            m = e4m3_scale(row16_max(m));
+            const Divide over(m);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) r[k][e] *= inv;
+            for (int e = 0; e < 8; ++e) r[k][e] = over(r[k][e]);
             if (left > 0) {
                 store8_e4m3<VEC, TPR == 0>(p.out8 + at + c, left, r[k]);
                 if ((j & 15) == 0) p.scales[row * ((D + 127) / 128) + c / 128] = m;
@@ -237,14 +259,14 @@ __device__ __forceinline__ void norm_row(const NormParams &p, int64_t row, int t
     }
     if (p.out8 && p.group == 0) {
         most = row_reduce<TPR, MaxOp>(most, s_red[1]);
-        const float scale = fmaxf(most * kE4m3Inv, kScaleFloor);
-        const float inv = __builtin_amdgcn_rcpf(scale);
+        const float scale = e4m3_scale(most);
+        const Divide over(scale);
         if (live && j == 0) p.scales[row] = scale;
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
             const int c = (k * tpr + j) * 8, left = live ? D - c : 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) r[k][e] *= inv;
+            for (int e = 0; e < 8; ++e) r[k][e] = over(r[k][e]);
             if (left > 0) store8_e4m3<VEC, TPR == 0>(p.out8 + at + c, left, r[k]);
         }
     }

@@ -224,3 +224,65 @@ def test_offsets_past_32_bits(gdn):
 def test_backward_of_many_rows(gdn, rows, D, dt):
     """Workgroups that take several rows each, and more than 512 of them."""
     test_backward(gdn, rows, D, dt, True)
+
+
+def e4m3_ties():
+    """448 and the 126 values halfway between neighbouring e4m3 values of 0 to 448."""
+    v = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).float()
+    return torch.cat([torch.tensor([448.0]), (v[1:] + v[:-1]) / 2, torch.tensor([-1.0])])
+
+
+@gpu
+@pytest.mark.parametrize("D", [128, 129, 512, 516, 1024, 4100, 16384])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("group", [0, 128])
+def test_quotients_at_ties(gdn, D, dt, group):
+    """out8 is y / scale rounded to nearest even: rows of +-1 have s = 1 and y = +-w, and with a
+    largest value of 448 c the scale is c and every quotient is a tie. Exact in every step: D / D,
+    eps below half a unit of 1, and c times a tie (5 bits) in 8 bits."""
+    assert torch.tensor(1.0 / D).mul(D) == 1  # the kernel's mean: the sum D times 1 / D in fp32
+    g = torch.Generator().manual_seed(D)
+    r = (torch.randint(0, 2, (3, D), generator=g) * 2 - 1).to(DT[dt])
+    ties = e4m3_ties()
+    for c in (1.0, 3.0, 5.0, 7.0, 1.5 * 2.0 ** 40, 1.75 * 2.0 ** -60):
+        w = (ties * c).repeat(-(-D // 128))[:D].to(DT[dt])
+        assert torch.equal(w.float(), (ties * c).repeat(-(-D // 128))[:D])
+        out, q, scale, _ = gdn.gdn_rms_norm(*dev(r, w), eps=2.0 ** -126, group=group,
+                                            want_out8=True)
+        assert torch.equal(out.cpu(), r * w)
+        assert (scale == c).all()
+        want = (r.float() * ties.repeat(-(-D // 128))[:D]).to(torch.float8_e4m3fn)
+        assert torch.equal(q.cpu().view(torch.uint8), want.view(torch.uint8)), c
+
+
+@gpu
+@pytest.mark.parametrize("rows,D", [(8192, 128), (5000, 200), (1000, 1024), (300, 5120), (99, 10001)],
+                         ids=str)
+@pytest.mark.parametrize("group", [0, 128])
+def test_quotients_are_those_of_a_division(gdn, rows, D, group):
+    """In fp32 `out` is y itself: scales and out8 are what divisions rounded once make of it."""
+    x, w, r = inputs(rows + D, rows, D, torch.float32)
+    out, q, scale, _ = gdn.gdn_rms_norm(*dev(x, w, r), group=group, want_out8=True)
+    y, q, scale = out.cpu(), q.cpu().view(torch.uint8), scale.cpu()
+    cols = group or D
+    for i, part in enumerate(y.split(cols, -1)):
+        s = (part.abs().amax(-1) / 448).clamp(min=2.0 ** -100)
+        assert torch.equal(scale[:, i], s)
+        want = (part / s[:, None]).to(torch.float8_e4m3fn).view(torch.uint8)
+        assert torch.equal(q[:, i * cols:i * cols + part.shape[-1]], want)
+
+
+@gpu
+def test_8bit_of_values_past_the_range(gdn):
+    """y past fp32's range (a large weight): an infinite scale, 0 for the finite values, NaN for the
+    infinite one; the other groups are as they were."""
+    for D, group in ((128, 0), (256, 128), (2048, 128), (2048, 0)):
+        x, w = torch.ones(2, D), torch.ones(D)
+        x[:, 5], w[5] = 3.0, 3e38
+        out, q, scale, _ = gdn.gdn_rms_norm(*dev(x, w), group=group, want_out8=True)
+        q, scale = q.cpu().float(), scale.cpu()
+        assert out[:, 5].isinf().all() and scale[:, 0].isinf().all()
+        n = group or D
+        assert q[:, 5].isnan().all() and (q[:, :5] == 0).all() and (q[:, 6:n] == 0).all()
+        if n < D:
+            assert (q[:, n:] == 448).all() and scale[:, 1:].isfinite().all()
