@@ -28,6 +28,7 @@ constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kMaxW = 32;
 constexpr int kList = 512;  // collected elements, at the most
 constexpr float kLog2e = 0x1.715476p+0f;
+constexpr float kFusedMax = 0x1p20f;  // largest |maximum| of a piece that is summed in one pass
 
 // A value's bits in an order of unsigned integers, -0 as +0.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -156,14 +157,16 @@ __global__ __launch_bounds__(kThreads, 8) void beam_piece_kernel(const DT *logit
     }
     uint64_t *out = best + (int64_t)blockIdx.x * W;
     const bool some = m > -__builtin_inff();
-    // The sum of e^(l - m) as 2^(l log2e - c), c the rounded m log2e. The terms
-    // that count have exponents near 0, so their own roundings are small; what c is
-    // off is common to all of them and taken out at the end. A NaN makes the sum
-    // NaN. Extreme rows (nothing but -inf, the lowest finite values, +inf) are
-    // summed from memory by l - m, which neither overflows for finite m nor hides
-    // a NaN or +inf: those make it NaN.
+    // The sum of e^(l - m) as 2^(l log2e - c), c the rounded m log2e: one fused
+    // multiply-add per exponent. The largest exponent is then what c is off, common
+    // to all terms and taken out at the end; below kFusedMax that is at most 2^-4.
+    // (It grows with m, and past 2^31 the sum would leave fp32's range.) Terms far
+    // below the largest are 0. A NaN makes the sum NaN. Rows of a larger maximum, a
+    // mask's fill over a whole piece above all, or of nothing but -inf, are summed
+    // from memory by l - m, which is exact where it counts and overflows only to
+    // -inf; a NaN or +inf there makes the sum NaN.
     float sum = 0.f;
-    if (fabsf(m) <= 1e38f) {
+    if (fabsf(m) <= kFusedMax) {
         const float c = m * kLog2e;
 #pragma unroll
         for (int j = 0; j < VECS; ++j)

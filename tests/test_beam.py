@@ -232,3 +232,53 @@ def test_offsets_past_32_bits(gdn):
     idx = torch.randperm(1500, generator=torch.Generator().manual_seed(2)).to(torch.int32).to(DEV)
     moved = gdn.gdn_gather_states(states, idx)
     assert torch.equal(moved[:, 0], idx.float()) and torch.equal(moved[:, -1], idx.float())
+
+
+FILLS = [1e5, 2.0 ** 20, 1.5e6, 1e9, 3e9, 1e10, 1e20, 1e30, 9e37, 2e38]
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("B,W,V", [(2, 4, 700), (1, 4, 2049), (1, 4, 6145), (8, 8, 32769)], ids=str)
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+def test_large_finite_logits(gdn, dt, B, W, V, sign):
+    """Masks and maxima of any finite size: over a whole row, a whole piece (of 2,048 logits, or of
+    8,192 with many rows) or a last piece of one logit. A beam stays alive: only NaN, +inf or nothing
+    but -inf end it."""
+    piece = 2048 if B * W * -(-V // 8192) < 256 else 8192
+    g = torch.Generator().manual_seed(V)
+    base = torch.randn(B, W, V, generator=g) * 3
+    scores = torch.randn(B, W, generator=g)
+    for size in FILLS:
+        fill = sign * size
+        cases = []
+        x = base.clone(); x[:, 1] = fill; cases.append(x)                  # noqa: E702 a whole row
+        x = base.clone(); x[:] = fill; cases.append(x)                     # noqa: E702 all of them
+        x = base.clone(); x[:, :, :min(piece, V - 1)] = fill; cases.append(x)  # noqa: E702 a piece
+        x = base.clone(); x[..., -1] = fill; cases.append(x)               # noqa: E702 the last one
+        if sign > 0:  # one best token of each beam: the W selected
+            cases = [cases[0], cases[1], cases[3]]
+        for x in cases:
+            x = x.to(DT[dt])
+            ns, tok, par = check(gdn, x, scores)
+            assert ns.isfinite().all()
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_large_logits_beside_nan_and_inf(gdn, dt):
+    """A NaN or +inf ends its beam also where the largest logit is extreme; -inf does not."""
+    V = 3000
+    g = torch.Generator().manual_seed(8)
+    base = torch.randn(1, 4, V, generator=g)
+    scores = torch.tensor([[-1.0, -2.0, -3.0, -4.0]])
+    for fill in (-1e10, -1e30, 1e10, 1e30):
+        for odd in (math.nan, math.inf, -math.inf):
+            x = base.clone()
+            x[0, 0] = fill
+            x[0, 0, 7] = odd
+            x = x.to(DT[dt])
+            check(gdn, x, scores)
+            # beside the others the live beam's best, -1 - log 2,999, may not be selected
+            ns, _, _ = check(gdn, x[:, :1], scores[:, :1])
+            assert ns.isfinite().all() == (odd == -math.inf)
