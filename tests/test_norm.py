@@ -286,3 +286,23 @@ def test_8bit_of_values_past_the_range(gdn):
         assert q[:, 5].isnan().all() and (q[:, :5] == 0).all() and (q[:, 6:n] == 0).all()
         if n < D:
             assert (q[:, n:] == 448).all() and scale[:, 1:].isfinite().all()
+
+
+@gpu
+@pytest.mark.parametrize("D", [128, 300, 1024, 2048, 9001])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("size,eps", [(0.0, 1e-30), (0.0, 2.0 ** -126), (1e-14, 1e-30),
+                                      (1e-17, 2.0 ** -126), (1.0, 2.0 ** -126), (1e14, 1e-6),
+                                      (1e16, 1e-6)], ids=str)
+def test_backward_of_small_and_large_rows(gdn, D, dt, size, eps):
+    """Every eps that is a normal number, and rows whose squares fp32 holds: s^3 alone would leave
+    its range. The largest |dx| here is s |w dy| < 2^63 * 20."""
+    dtype = DT[dt]
+    r, w, _ = inputs(D, 5, D, dtype, False)
+    r = (r.float() * size).to(dtype)
+    dy = torch.randn(5, D, generator=torch.Generator().manual_seed(3)).to(dtype)
+    dx, dw = gdn.gdn_rms_norm_backward(*dev(dy, r, w), eps=eps)
+    want, want_w, mag, mag_w = norm_backward64(dy, r, w, None, float(torch.tensor(eps)))
+    tol = 2 * REL * mag + (half_step(dtype) * want.abs() * (1 + REL) if dt == "bf16" else 0)
+    assert ((dx.cpu().double() - want).abs() <= tol + 1e-37).all()
+    assert ((dw.cpu().double() - want_w).abs() <= (REL + U32 * 45) * mag_w + 1e-37).all()
