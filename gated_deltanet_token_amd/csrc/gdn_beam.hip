@@ -95,16 +95,18 @@ __device__ __forceinline__ uint32_t wave_bound(uint32_t x, int want, int low) {
 // again so that they do not cost the registers for that.
 template <typename DT, int VECS>
 __global__ __launch_bounds__(kThreads, 8) void beam_piece_kernel(const DT *logits, int64_t V, int W,
-                                                              int npieces, PieceSum *sums,
-                                                              uint64_t *best) {
+                                                                 int npieces, uint32_t total,
+                                                                 PieceSum *sums, uint64_t *best) {
     constexpr int kPiece = VECS * 8 * kThreads;
     __shared__ uint64_t s_list[kList];
     __shared__ float s_top[kWaves], s_sum[kWaves];
     __shared__ uint32_t s_bound[kWaves];
     __shared__ int s_count;
 
-    const int64_t row = blockIdx.x / npieces;
-    const int piece = blockIdx.x - (int)(row * npieces);
+    const uint32_t wg = workgroup();
+    if (wg >= total) return;
+    const int64_t row = wg / npieces;
+    const int piece = wg - (int)(row * npieces);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const DT *from = logits + row * V + (int64_t)piece * kPiece;
     const uint32_t first = (uint32_t)piece * kPiece;  // the piece's first token
@@ -155,7 +157,7 @@ __global__ __launch_bounds__(kThreads, 8) void beam_piece_kernel(const DT *logit
         m = fmaxf(m, s_top[i]);
         ob = max(ob, s_bound[i]);
     }
-    uint64_t *out = best + (int64_t)blockIdx.x * W;
+    uint64_t *out = best + (int64_t)wg * W;
     const bool some = m > -__builtin_inff();
     // The sum of e^(l - m) as 2^(l log2e - c), c the rounded m log2e: one fused
     // multiply-add per exponent. The largest exponent is then what c is off, common
@@ -211,7 +213,7 @@ __global__ __launch_bounds__(kThreads, 8) void beam_piece_kernel(const DT *logit
         float all = s_sum[0];
 #pragma unroll
         for (int i = 1; i < kWaves; ++i) all += s_sum[i];
-        sums[blockIdx.x] = PieceSum{all != all ? all : m, all};
+        sums[wg] = PieceSum{all != all ? all : m, all};
     }
     const int count = s_count;
     if ((picky || few) && count <= kList) {
@@ -322,7 +324,8 @@ __global__ __launch_bounds__(THREADS) void beam_join_kernel(BeamParams p, int np
     __shared__ uint32_t s_bound[kWaves];
     __shared__ int s_count;
 
-    const int b = blockIdx.x, W = p.W, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    if (workgroup() >= (uint32_t)p.B) return;
+    const int b = workgroup(), W = p.W, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t V = p.V;
     const int per = npieces * W, n = W * per;  // candidates of a beam, and all
     const uint64_t *keys = best + (int64_t)b * n;
@@ -442,9 +445,11 @@ __global__ __launch_bounds__(THREADS) void beam_join_kernel(BeamParams p, int np
 // read and written, parents that several beams share coming from cache).
 __global__ __launch_bounds__(256) void gather_kernel(const u32x4 *src, int64_t num_src,
                                                      const int32_t *index, u32x4 *dst,
-                                                     int64_t row_vecs, int parts) {
-    const int64_t row = blockIdx.x / parts;
-    const int part = blockIdx.x - (int)(row * parts);
+                                                     int64_t row_vecs, int parts, uint32_t total) {
+    const uint32_t wg = workgroup();
+    if (wg >= total) return;
+    const int64_t row = wg / parts;
+    const int part = wg - (int)(row * parts);
     const int64_t from = index[row];
     const int64_t v0 = (int64_t)part * 1024 + threadIdx.x;
     u32x4 *to = dst + row * row_vecs;
@@ -487,7 +492,10 @@ hipError_t launch_beam(const BeamParams &p, int dtype, void *ws, hipStream_t str
     PieceSum *sums = static_cast<PieceSum *>(ws);
     uint64_t *best = reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + keys_offset(pieces));
     const bool few = piece_vecs(rows, p.V) == 1;
-#define GDN_BEAM_LAUNCH(DT, VECS)                                                                    hipLaunchKernelGGL((beam_piece_kernel<DT, VECS>), dim3((unsigned)pieces), dim3(kThreads), 0,                        stream, static_cast<const DT *>(p.logits), p.V, p.W, (int)np, sums, best)
+#define GDN_BEAM_LAUNCH(DT, VECS)                                                              \
+    hipLaunchKernelGGL((beam_piece_kernel<DT, VECS>), grid_of(pieces, kThreads), dim3(kThreads), 0, \
+                       stream, static_cast<const DT *>(p.logits), p.V, p.W, (int)np,              \
+                       (uint32_t)pieces, sums, best)
     if (dtype == 1) {
         if (few)
             GDN_BEAM_LAUNCH(__bf16, 1);
@@ -504,13 +512,13 @@ hipError_t launch_beam(const BeamParams &p, int dtype, void *ws, hipStream_t str
     if (e != hipSuccess) return e;
     // a wave per beam where that is enough of them: their sums take the longest
     if (p.W > 4 && p.W <= 8 && np * p.W * p.W <= 2048)
-        hipLaunchKernelGGL((beam_join_kernel<512, 4>), dim3((unsigned)p.B), dim3(512), 0, stream,
+        hipLaunchKernelGGL((beam_join_kernel<512, 4>), grid_of(p.B, 512), dim3(512), 0, stream,
                            p, (int)np, sums, best);
     else if (np * p.W * p.W <= 1024)
-        hipLaunchKernelGGL((beam_join_kernel<256, 4>), dim3((unsigned)p.B), dim3(256), 0, stream,
+        hipLaunchKernelGGL((beam_join_kernel<256, 4>), grid_of(p.B, 256), dim3(256), 0, stream,
                            p, (int)np, sums, best);
     else
-        hipLaunchKernelGGL((beam_join_kernel<1024, 8>), dim3((unsigned)p.B), dim3(1024), 0,
+        hipLaunchKernelGGL((beam_join_kernel<1024, 8>), grid_of(p.B, 1024), dim3(1024), 0,
                            stream, p, (int)np, sums, best);
     return hipGetLastError();
 }
@@ -519,9 +527,9 @@ hipError_t launch_gather(const void *src, int64_t num_src, const int32_t *index,
                          int64_t rows, int64_t row_bytes, hipStream_t stream) {
     if (rows == 0 || row_bytes == 0) return hipSuccess;
     const int parts = (int)((row_bytes + 16383) / 16384);
-    hipLaunchKernelGGL(gather_kernel, dim3((unsigned)(rows * parts)), dim3(256), 0, stream,
+    hipLaunchKernelGGL(gather_kernel, grid_of(rows * parts, 256), dim3(256), 0, stream,
                        static_cast<const u32x4 *>(src), num_src, index, static_cast<u32x4 *>(dst),
-                       row_bytes / 16, parts);
+                       row_bytes / 16, parts, (uint32_t)(rows * parts));
     return hipGetLastError();
 }
 

@@ -282,7 +282,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p) {
     const int tpr = row_threads<TPR>();
     const int j = TPR == 0 ? threadIdx.x : threadIdx.x % tpr;
     const int per = TPR == 0 ? 1 : blockDim.x / tpr;
-    const int64_t row0 = (int64_t)blockIdx.x * per * NROWS + (TPR == 0 ? 0 : threadIdx.x / tpr);
+    const int64_t row0 = (int64_t)workgroup() * per * NROWS + (TPR == 0 ? 0 : threadIdx.x / tpr);
     NormRow<DT, VEC, TPR, CH> rows[NROWS];
 #pragma unroll
     for (int i = 0; i < NROWS; ++i)
@@ -502,14 +502,14 @@ struct RunNorm {
         if constexpr (TPR != 0) {
             if (p.rows >= (int64_t)n.per * 2 * 4096) {
                 hipLaunchKernelGGL((norm_kernel<DT, VEC, TPR, CH, 2>),
-                                   dim3((unsigned)((p.rows + 2 * n.per - 1) / (2 * n.per))),
+                                   grid_of((p.rows + 2 * n.per - 1) / (2 * n.per), n.threads),
                                    dim3(n.threads), 0, stream, p);
                 return hipGetLastError();
             }
         }
         hipLaunchKernelGGL((norm_kernel<DT, VEC, TPR, CH, 1>),
-                           dim3((unsigned)((p.rows + n.per - 1) / n.per)), dim3(n.threads), 0,
-                           stream, p);
+                           grid_of((p.rows + n.per - 1) / n.per, n.threads), dim3(n.threads),
+                           0, stream, p);
         return hipGetLastError();
     }
 };

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "../../include/gdn.h"
+#include "gdn_grid.hpp"
 
 namespace gdn {
 

@@ -29,7 +29,7 @@ struct ScanTile {
 template <bool BACK>
 __device__ __forceinline__ ScanTile take_tile(const ScanParams &p, const ScanSplit &sp, int ncb,
                                               int *s_take) {
-    const int chain = sp.runs.chain(blockIdx.x % sp.runs.grid);
+    const int chain = sp.runs.chain(workgroup() % sp.runs.grid);
     if (chain < 0) return ScanTile{-1, 0, 0, 0};
     if (threadIdx.x == 0) {
         s_take[0] = (int)__hip_atomic_fetch_add(sp.ticket + chain, 1u, __ATOMIC_RELAXED,
@@ -71,7 +71,7 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_forward_k
     __shared__ float s_a[G][C], s_h[G][C];
 
     __shared__ int s_take[3];
-    const int pair = SPLIT > 0 ? 0 : sp.runs.chain(blockIdx.x);
+    const int pair = SPLIT > 0 ? 0 : sp.runs.chain(workgroup());
     ScanTile mine{pair / ncb, pair % ncb, 0, 0};
     if constexpr (SPLIT > 0) mine = take_tile<false>(p, sp, ncb, s_take);
     if (SPLIT > 0 ? mine.n < 0 : pair < 0) return;
@@ -197,7 +197,7 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads), 4) void scan_backwa
     __shared__ float s_a[G][C], s_h[G][C], s_k[G][C];
 
     __shared__ int s_take[3];
-    const int pair = SPLIT > 0 ? 0 : sp.runs.chain(blockIdx.x);
+    const int pair = SPLIT > 0 ? 0 : sp.runs.chain(workgroup());
     ScanTile mine{pair / ncb, pair % ncb, 0, 0};
     if constexpr (SPLIT > 0) mine = take_tile<true>(p, sp, ncb, s_take);
     if (SPLIT > 0 ? mine.n < 0 : pair < 0) return;
@@ -389,7 +389,7 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads), 4) void scan_backwa
 template <typename DT, int VEC, bool TIED, bool LOGITS>
 __global__ __launch_bounds__(256) void scan_decode_kernel(ScanDecodeParams p) {
     const int per = (p.D + VEC - 1) / VEC;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t i = (int64_t)workgroup() * 256 + threadIdx.x;
     const int64_t b = i / per;
     if (b >= p.B) return;
     const int c0 = (int)(i - b * per) * VEC;
@@ -560,7 +560,7 @@ struct RunForward {
     template <typename DT, int VEC, bool TIED, bool LOGITS> hipError_t run() const {
         const int ncb = column_blocks<DT, VEC>(p.D);
         const dim3 block(ScanShape<DT, VEC>::kThreads);
-        const dim3 grid(sp.slots > 0 ? (unsigned)(sp.per_chain * sp.runs.grid) : sp.runs.grid);
+        const dim3 grid = grid_of((sp.slots > 0 ? sp.per_chain : 1) * sp.runs.grid, block.x);
         if (sp.slots > 0 && sp.deep > 1)
             hipLaunchKernelGGL((scan_forward_kernel<DT, VEC, TIED, LOGITS, kDeep>), grid, block, 0,
                                stream, p, ncb, sp);
@@ -581,7 +581,7 @@ struct RunBackward {
     template <typename DT, int VEC, bool TIED, bool LOGITS> hipError_t run() const {
         const int ncb = column_blocks<DT, VEC>(p.D);
         const dim3 block(ScanShape<DT, VEC>::kThreads);
-        const dim3 grid(sp.slots > 0 ? (unsigned)(sp.per_chain * sp.runs.grid) : sp.runs.grid);
+        const dim3 grid = grid_of((sp.slots > 0 ? sp.per_chain : 1) * sp.runs.grid, block.x);
         if (sp.slots > 0 && sp.deep > 1)
             hipLaunchKernelGGL((scan_backward_kernel<DT, VEC, TIED, LOGITS, kDeep>), grid, block, 0,
                                stream, p, ncb, sp);
@@ -601,7 +601,7 @@ struct RunDecode {
     template <typename DT, int VEC, bool TIED, bool LOGITS> hipError_t run() const {
         const int64_t threads = (int64_t)p.B * ((p.D + VEC - 1) / VEC);
         hipLaunchKernelGGL((scan_decode_kernel<DT, VEC, TIED, LOGITS>),
-                           dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, p);
+                           grid_of((threads + 255) / 256, 256), dim3(256), 0, stream, p);
         return hipGetLastError();
     }
 };

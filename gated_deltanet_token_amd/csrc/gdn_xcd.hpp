@@ -33,11 +33,12 @@ struct XcdRuns {
         return XcdRuns{(int32_t)chains, (int32_t)run, (int32_t)full,
                        (int32_t)(full + (chains - full + kXcds - 1) / kXcds * kXcds)};
     }
-    // The chain of workgroup i of `grid`, or -1.
-    GDN_HOST_DEVICE int chain(int i) const {
-        if (run == 0) return i;
+    // The chain of workgroup i, or -1 (among the first `grid`, and for all behind them).
+    GDN_HOST_DEVICE int chain(uint32_t i) const {
+        if (i >= (uint32_t)grid) return -1;
+        if (run == 0) return (int)i;
         const int x = i % kXcds, j = i / kXcds;
-        if (i < full) return (j / run * kXcds + x) * run + j % run;
+        if (i < (uint32_t)full) return (j / run * kXcds + x) * run + j % run;
         const int k = j - full / kXcds, each = (chains - full) / kXcds;
         const int more = (chains - full) % kXcds;
         if (k >= each + (x < more)) return -1;
