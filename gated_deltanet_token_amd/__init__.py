@@ -369,10 +369,18 @@ def gdn_decode_multi(q, k, v, alpha, beta, state_pool, src_slot, dst_slot, *, ou
     return out, step_states
 
 
+def _keep_for(stream, *tensors):
+    """Memory of tensors that were made on another stream: freed by their owner,
+    it is not handed out again before what `stream` has been given so far is done."""
+    for t in tensors:
+        if isinstance(t, torch.Tensor):
+            t.record_stream(stream)
+
+
 def _on_stream(first):
     """Runs a call on the device of its argument `first` and on its `stream`
     argument: torch allocates and the library launches there, whatever the
-    current device and stream are."""
+    current device and stream are. The call's tensors are kept for that stream."""
     def wrap(fn):
         @functools.wraps(fn)
         def call(*args, stream=None, **kw):
@@ -389,7 +397,10 @@ def _on_stream(first):
             elif stream.device_index != index:
                 raise ValueError(f"stream is on device {stream.device_index}, {first} on {index}")
             with torch.cuda.stream(stream):
-                return fn(*args, **kw)
+                out = fn(*args, **kw)
+            if stream != torch.cuda.current_stream(index):
+                _keep_for(stream, *args, *kw.values())
+            return out
         return call
     return wrap
 
@@ -517,7 +528,8 @@ def gdn_scan_prefill(x, alpha, beta=None, initial_state=None, *, out=None, final
     receiving the state after every whole block of 64 * prefix_interval tokens
     (gdn_scan_backward takes them with an interval of 1 or 2). `stream` (a
     torch.cuda.Stream, here and in the calls below): where to run, the current
-    one by default."""
+    one by default. It is for the caller to let it wait for the inputs; their
+    memory may be freed at once. Outputs made by the call belong to it."""
     return _scan_forward(x, alpha, beta, None, initial_state, out, final_state, want_final_state,
                          prefix_states, prefix_interval, flags, workspace)
 

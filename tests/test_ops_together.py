@@ -275,3 +275,37 @@ def test_scan_after_other_work_on_its_rows(gdn):
     assert h.data_ptr() == out.data_ptr() and (out[0, T:] == 9.0).all()
     want, err = scan64(x[0].cpu(), a[0].cpu(), b[0].cpu(), None, True)
     assert ((h[0].cpu().double() - want).abs() <= K * U32 * err + 1e-37).all()
+
+
+def freed_after_the_call(call, *tensors):
+    """call(stream, tensors...) on a busy side stream, its inputs freed at once and their memory
+    written again on the current stream: the results are those of an undisturbed call."""
+    want = [t.clone() for t in call(None, *[t.clone() for t in tensors]) if t is not None]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    mine = [t.clone() for t in tensors]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)  # some 0.1 s
+    got = [t for t in call(side, *mine) if t is not None]
+    del mine
+    other = [torch.empty_like(t) for t in tensors]
+    for t in other:
+        t.view(torch.uint8).fill_(0x3F)
+    torch.cuda.synchronize()
+    for p, q in zip(got, want):
+        assert torch.equal(p, q)
+
+
+def test_inputs_freed_after_a_call_on_another_stream(gdn):
+    s = make(50)
+    freed_after_the_call(lambda st, x, w, r: gdn.gdn_rms_norm(x, w, residual=r, stream=st),
+                         s["x"], s["w"], s["res"])
+    freed_after_the_call(lambda st, dy, r, w: gdn.gdn_rms_norm_backward(dy, r, weight=w, stream=st),
+                         s["dy"], s["x"], s["w"])
+    freed_after_the_call(lambda st, x, a, b, h: gdn.gdn_scan_prefill(x, a, b, h, stream=st),
+                         s["x"], s["a"], s["b"], s["h0"])
+    freed_after_the_call(lambda st, lg, sc: gdn.gdn_beam_select(lg, scores=sc, stream=st),
+                         s["logits"], s["score"])
+    freed_after_the_call(lambda st, p, i: [gdn.gdn_gather_states(p, i, stream=st)],
+                         s["pool"], s["src"])
