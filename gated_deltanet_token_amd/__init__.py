@@ -151,6 +151,25 @@ def _stream(device, stream):
     return stream if stream is not None else torch.cuda.current_stream(device)
 
 
+def _keep_for(stream, *tensors):
+    """Memory of tensors that were made on another stream: freed by their owner,
+    it is not handed out again before what `stream` has been given so far is done."""
+    for t in tensors:
+        if isinstance(t, torch.Tensor):
+            t.record_stream(stream)
+
+
+def _keeps(fn):
+    """Keeps a call's tensors, results among them, for its `stream` argument."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        out = fn(*args, stream=stream, **kw)
+        if stream is not None and stream != torch.cuda.current_stream(stream.device):
+            _keep_for(stream, *args, *kw.values(), *(out if isinstance(out, tuple) else (out,)))
+        return out
+    return call
+
+
 def gdn_prefill_workspace_size(num_seqs, tokens, Hk, Hv, Dk, Dv, dtype, packed) -> int:
     """Workspace bytes the prefill calls can use (0: they would not use one)."""
     code = _dtype_code(torch.empty(0, dtype=dtype)) if isinstance(dtype, torch.dtype) else dtype
@@ -193,6 +212,7 @@ def _prefix(prefix_states, prefix_interval, rows, Hv, Dv, Dk, dev):
     return prefix_states, int(prefix_interval)
 
 
+@_keeps
 def gdn_prefill_chunked(q, k, v, alpha, beta, initial_state=None, *, out=None,
                         final_state=None, scale: float = 1.0, want_final_state: bool = True,
                         prefix_states=None, prefix_interval: int = 0, flags: int = 0,
@@ -233,6 +253,7 @@ def gdn_prefill_chunked(q, k, v, alpha, beta, initial_state=None, *, out=None,
     return out, final_state
 
 
+@_keeps
 def gdn_prefill_chunked_noalloc(q, k, v, alpha, beta, initial_state=None, *, out=None,
                                 final_state=None, scale: float = 1.0,
                                 want_final_state: bool = True, prefix_states=None,
@@ -269,6 +290,7 @@ def gdn_prefill_chunked_noalloc(q, k, v, alpha, beta, initial_state=None, *, out
     return out, final_state
 
 
+@_keeps
 def gdn_varlen_prefill(q, k, v, alpha, beta, cu_seqlens, initial_state=None, *, out=None,
                        final_state=None, scale: float = 1.0, want_final_state: bool = True,
                        prefix_states=None, prefix_interval: int = 0, flags: int = 0,
@@ -309,6 +331,7 @@ def gdn_varlen_prefill(q, k, v, alpha, beta, cu_seqlens, initial_state=None, *, 
     return out, final_state
 
 
+@_keeps
 def gdn_decode_step(q, k, v, alpha, beta, state, *, out=None, scale: float = 1.0, flags: int = 0,
                     stream=None):
     """One token per sequence; `state` [B,Hv,D,D] fp32 is updated in place.
@@ -332,6 +355,7 @@ def gdn_decode_step(q, k, v, alpha, beta, state, *, out=None, scale: float = 1.0
     return out
 
 
+@_keeps
 def gdn_decode_multi(q, k, v, alpha, beta, state_pool, src_slot, dst_slot, *, out=None,
                      step_states=None, want_step_states: bool = False, scale: float = 1.0,
                      flags: int = 0, stream=None):
@@ -367,14 +391,6 @@ def gdn_decode_multi(q, k, v, alpha, beta, state_pool, src_slot, dst_slot, *, ou
         state_pool.shape[0], _ptr(src_slot), _ptr(dst_slot), _ptr(out), _ptr(step_states), B, K,
         Hk, Hv, Dk, Dv, _dtype_code(q), float(scale), int(flags), _stream(dev, stream).cuda_stream))
     return out, step_states
-
-
-def _keep_for(stream, *tensors):
-    """Memory of tensors that were made on another stream: freed by their owner,
-    it is not handed out again before what `stream` has been given so far is done."""
-    for t in tensors:
-        if isinstance(t, torch.Tensor):
-            t.record_stream(stream)
 
 
 def _on_stream(first):

@@ -309,3 +309,24 @@ def test_inputs_freed_after_a_call_on_another_stream(gdn):
                          s["logits"], s["score"])
     freed_after_the_call(lambda st, p, i: [gdn.gdn_gather_states(p, i, stream=st)],
                          s["pool"], s["src"])
+
+
+def test_inputs_of_the_mixer_freed_after_a_call_on_another_stream(gdn):
+    g = torch.Generator().manual_seed(51)
+    r = lambda *s: torch.randn(*s, generator=g).to(DEV)  # noqa: E731
+    B, T, Hk, Hv, D = 2, 200, 2, 4, 64
+    q, k, v = 0.1 * r(B, T, Hk, D), 0.1 * r(B, T, Hk, D), r(B, T, Hv, D)
+    al, be = torch.sigmoid(r(B, T, Hv)), torch.sigmoid(r(B, T, Hv))
+    freed_after_the_call(lambda st, *t: gdn.gdn_prefill_chunked(*t, stream=st), q, k, v, al, be)
+    cu = torch.tensor([0, 150, 400], dtype=torch.int32, device=DEV)
+    flat = [t.flatten(0, 1) for t in (q, k, v, al, be)]
+    freed_after_the_call(lambda st, *t: gdn.gdn_varlen_prefill(*t, stream=st), *flat, cu)
+    freed_after_the_call(lambda st, *t: gdn.gdn_prefill_chunked_noalloc(*t, stream=st),
+                         q, k, v, al, be)
+    one = [t[:, 0].contiguous() for t in (q, k, v, al, be)]
+    freed_after_the_call(lambda st, *t: [gdn.gdn_decode_step(*t, stream=st)], *one,
+                         r(B, Hv, D, D))
+    ids = torch.arange(B, dtype=torch.int32, device=DEV)
+    freed_after_the_call(lambda st, *t: gdn.gdn_decode_multi(*t, stream=st),
+                         *[t[:, :3].contiguous() for t in (q, k, v, al, be)], r(B, Hv, D, D), ids,
+                         ids)
