@@ -130,6 +130,13 @@ def _dtype_code(t: torch.Tensor) -> int:
     raise TypeError(f"q, k, v must be bfloat16 or float32, got {t.dtype}")
 
 
+_INT32 = 0x7FFFFFFF  # the library takes sizes in 32 bits; ctypes drops the bits above
+
+
+def _out_of_range(**values):
+    raise ValueError("out of range: " + ", ".join(f"{k} = {v}" for k, v in values.items()))
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -208,6 +215,8 @@ def _prefix(prefix_states, prefix_interval, rows, Hv, Dv, Dk, dev):
         return None, 0
     if int(prefix_interval) < 1:
         raise ValueError("prefix_interval must be >= 1 with prefix_states")
+    if int(prefix_interval) > _INT32:
+        _out_of_range(prefix_interval=prefix_interval)
     _need(prefix_states, "prefix_states", torch.float32, (rows, Hv, Dv, Dk), dev)
     return prefix_states, int(prefix_interval)
 
@@ -470,6 +479,8 @@ def _scratch(workspace, size, index, like):
 def gdn_scan_workspace_size(num_seqs, tokens, D, dtype, packed) -> int:
     """Workspace bytes the scan calls can use (0: they would not use one)."""
     code = _dtype_code(torch.empty(0, dtype=dtype)) if isinstance(dtype, torch.dtype) else dtype
+    if max(num_seqs, D) > _INT32:
+        return 0
     return int(load_library().gdn_scan_workspace_size(num_seqs, tokens, D, code,
                                                       int(bool(packed))))
 
@@ -486,6 +497,8 @@ def _scan_sizes(x, cu, index):
 
 def _scan_prefix(prefix, interval, n, tokens, packed, D, index):
     interval = int(interval)
+    if not -_INT32 <= interval <= _INT32:
+        _out_of_range(prefix_interval=interval)
     if prefix is not None:
         if interval < 1:
             raise ValueError("prefix_interval must be >= 1 with prefix_states")
@@ -504,6 +517,8 @@ def _scan_forward(x, alpha, beta, cu, h0, out, final, want_final, prefix, interv
     if beta is not None:
         _like(beta, "beta", dt, shape, index)
     n, tokens, D = _scan_sizes(x, cu, index)
+    if n > _INT32 or D > _INT32 or flags >> 32:
+        _out_of_range(sequences=n, D=D, flags=flags)
     if h0 is not None:
         _like(h0, "initial_state", torch.float32, (n, D), index)
     interval = _scan_prefix(prefix, interval, n, tokens, packed, D, index)
@@ -575,6 +590,8 @@ def _scan_backward(dout, x, alpha, beta, cu, h0, prefix, interval, dfinal, dx, d
     elif dbeta is not None:
         raise ValueError("dbeta must be None with tied gates (beta None)")
     n, tokens, D = _scan_sizes(x, cu, index)
+    if n > _INT32 or D > _INT32 or flags >> 32:
+        _out_of_range(sequences=n, D=D, flags=flags)
     for t, name in ((h0, "initial_state"), (dfinal, "dfinal"), (dinitial, "dinitial")):
         if t is not None:
             _like(t, name, torch.float32, (n, D), index)
@@ -652,6 +669,8 @@ def gdn_scan_decode(x, alpha, beta, state_pool, src_slot, dst_slot, *, out=None,
     if not isinstance(state_pool, torch.Tensor) or state_pool.dim() != 2:
         raise ValueError("state_pool must be a tensor of shape [num_slots, D]")
     num_slots = state_pool.shape[0]
+    if max(B, K, D, num_slots) > _INT32 or flags >> 32:
+        _out_of_range(B=B, K=K, D=D, num_slots=num_slots, flags=flags)
     _like(state_pool, "state_pool", torch.float32, (num_slots, D), index)
     _like(src_slot, "src_slot", torch.int32, (B,), index)
     _like(dst_slot, "dst_slot", torch.int32, (B,), index)
@@ -675,6 +694,8 @@ def _rows(t, name):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     D = t.shape[-1]
+    if D > _INT32:
+        _out_of_range(D=D)
     return _dtype_code(t), t.get_device(), t.numel() // D, D
 
 
@@ -775,6 +796,8 @@ def gdn_beam_select(logits, scores, *, finished=None, eos: int = -1, beam_slots=
     lib = _lib or load_library()
     code, index, (B, W, V) = _start(logits, "logits", 3)
     shape = (B, W)
+    if max(B, W, abs(eos)) > _INT32:
+        _out_of_range(B=B, W=W, eos=eos)
     _like(scores, "scores", torch.float32, shape, index)
     if finished is not None:
         _like(finished, "finished", torch.uint8, shape, index)

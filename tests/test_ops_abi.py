@@ -246,3 +246,43 @@ def test_binding_refuses_bad_tensors():
         g.gdn_gather_states(x, torch.zeros(2, dtype=torch.int64))
     with pytest.raises(ValueError):
         g.gdn_gather_states(x, torch.zeros(2, dtype=torch.int32))
+
+
+def test_binding_refuses_what_32_bits_do_not_hold():
+    """ctypes drops the upper bits of an integer: a prefix interval of 2^32 + 1 would ask for no
+    rows here and write every 64 tokens in the library."""
+    import gated_deltanet_token_amd as g
+    wrap = 2 ** 32
+    x = torch.zeros(1, 200, 8)
+    none = torch.zeros(0, 8)
+    for kw in ({"prefix_states": none, "prefix_interval": wrap + 1}, {"flags": wrap},
+               {"flags": -1}):
+        with pytest.raises(ValueError, match="out of range"):
+            g.gdn_scan_prefill(x, x, x, **kw)
+        with pytest.raises(ValueError, match="out of range"):
+            g.gdn_scan_backward(x, x, x, x, **kw)
+    cu = torch.tensor([0, 200], dtype=torch.int32)
+    with pytest.raises(ValueError, match="out of range"):
+        g.gdn_scan_varlen_prefill(x[0], x[0], x[0], cu, prefix_states=torch.zeros(1, 8),
+                                  prefix_interval=wrap + 1)
+    e = torch.zeros(1, 0, wrap + 8)
+    with pytest.raises(ValueError, match="out of range"):
+        g.gdn_scan_prefill(e, e, e)
+    with pytest.raises(ValueError, match="out of range"):
+        g.gdn_rms_norm(e, torch.zeros(8))
+    slots = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="out of range"):
+        g.gdn_scan_decode(x, x, x, torch.zeros(2, 8), slots, slots, flags=wrap)
+    with pytest.raises(ValueError, match="out of range"):
+        g.gdn_scan_decode(e, e, e, torch.zeros(0, wrap + 8), slots, slots)
+    with pytest.raises(ValueError, match="out of range"):
+        g.gdn_beam_select(x, torch.zeros(1, 200), eos=wrap + 3)
+    assert g.gdn_scan_workspace_size(wrap + 1, 4096, 64, torch.float32, False) == 0
+    assert g.gdn_scan_workspace_size(1, 4096, wrap + 64, torch.float32, False) == 0
+    q, ab = torch.zeros(1, 200, 1, 64), torch.zeros(1, 200, 1)
+    pre = torch.zeros(0, 1, 64, 64)
+    with pytest.raises(ValueError, match="out of range"):
+        g.gdn_prefill_chunked(q, q, q, ab, ab, prefix_states=pre, prefix_interval=wrap + 1)
+    with pytest.raises(ValueError, match="out of range"):
+        g.gdn_varlen_prefill(q[0], q[0], q[0], ab[0], ab[0], cu, prefix_states=pre[:0].new_zeros(
+            1, 1, 64, 64), prefix_interval=wrap + 1)
