@@ -37,9 +37,9 @@ __device__ __forceinline__ ScanTile take_tile(const ScanParams &p, const ScanSpl
         s_take[1] = 0;
     }
     __syncthreads();
-    int64_t k = __builtin_amdgcn_readfirstlane(s_take[0]);  // uniform, and known to be
-    if (k < 0 || k >= sp.per_chain) return ScanTile{-1, 0, 0, 0};
-    if (BACK) k = sp.per_chain - 1 - k;
+    // uniform, and known to be
+    const int64_t k = counted_tile(__builtin_amdgcn_readfirstlane(s_take[0]), sp.per_chain, BACK);
+    if (k < 0) return ScanTile{-1, 0, 0, 0};
     ScanTile t;
     if (p.cu) {
         t.cb = chain;

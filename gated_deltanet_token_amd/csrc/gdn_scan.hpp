@@ -3,7 +3,7 @@
 #pragma once
 #include "gdn_device.hpp"
 #include "gdn_ops_launch.hpp"
-#include "gdn_xcd.hpp"
+#include "gdn_split.hpp"
 
 namespace gdn {
 
@@ -179,11 +179,7 @@ template <typename DT, int VEC> struct ScanShape {
 __device__ __forceinline__ void scan_bounds(const ScanParams &p, int n, int64_t &base,
                                             int64_t &len) {
     if (p.cu) {
-        int64_t lo = p.cu[n], hi = p.cu[n + 1];
-        lo = lo < 0 ? 0 : (lo > p.total ? p.total : lo);
-        hi = hi < lo ? lo : (hi > p.total ? p.total : hi);
-        base = lo;
-        len = hi - lo;
+        clamp_sequence(p.cu[n], p.cu[n + 1], p.total, base, len);
     } else {
         base = (int64_t)n * p.T;
         len = p.T;
@@ -225,9 +221,10 @@ __device__ __forceinline__ int64_t scan_block_ending(const ScanParams &p, int64_
 // only for tiles of its chain that were taken before it, by workgroups that run
 // already and in turn wait only for earlier ones, and every taken tile
 // publishes: every wait ends. A wait is bounded all the same (about 3 s, where
-// a right one takes microseconds) and a count from the counter is checked: a
-// caller that lets two calls overlap on one workspace gets NaN or tiles left
-// out, and neither a hang nor an access out of range.
+// a right one takes microseconds) and a count from the counter is checked: two
+// calls that a caller lets overlap on one workspace neither hang nor leave the
+// buffers. Their results are undefined: NaN, tiles left out, or finite values
+// made from the other call's words.
 struct ScanSplit {
     uint32_t *ticket;  // [chains]
     uint64_t *map;     // [slots][width], SPLIT > 1: A low, H high
@@ -239,7 +236,6 @@ struct ScanSplit {
     int64_t per_chain; // workgroups that take a chain's tiles
 };
 
-constexpr uint32_t kAbsent = 0xFFFFFFFFu;
 constexpr int kScanSpins = 1 << 22;  // looks of about 0.7 us
 
 // A value's bits; any NaN becomes the plain one, never kAbsent.
@@ -266,51 +262,21 @@ __device__ __forceinline__ void publish_map(const ScanSplit &sp, int64_t slot, i
 template <int SPLIT>
 __device__ __forceinline__ float find_state(const ScanSplit &sp, int64_t at, int64_t step,
                                             int32_t ahead, int col) {
-    if constexpr (SPLIT == 1) {
-        const uint32_t *p = sp.state + at * sp.width + col;
-        for (int spin = 0; spin < kScanSpins; ++spin) {
-            const uint32_t w = observe(p);
-            if (w != kAbsent) return __builtin_bit_cast(float, w);
-            __builtin_amdgcn_s_sleep(1);
-        }
-    } else {
-        for (int spin = 0; spin < kScanSpins; ++spin) {
-            uint32_t state[SPLIT];
-            uint64_t map[SPLIT];
-#pragma unroll
-            for (int j = 0; j < SPLIT; ++j) {
-                const int64_t i = (at + (j < ahead ? j : ahead - 1) * step) * sp.width + col;
-                state[j] = observe(sp.state + i);
-                map[j] = observe(sp.map + i);
-            }
-            float c = 0.f;
-            bool found = false;
-#pragma unroll
-            for (int j = SPLIT - 1; j >= 0; --j) {
-                if (j >= ahead) continue;
-                if (state[j] != kAbsent) {
-                    c = __builtin_bit_cast(float, state[j]);
-                    found = true;
-                } else {
-                    found &= map[j] != ~(uint64_t)0;
-                    c = fmaf(__builtin_bit_cast(float, (uint32_t)map[j]), c,
-                             __builtin_bit_cast(float, (uint32_t)(map[j] >> 32)));
-                }
-            }
-            if (found) return c;
-            __builtin_amdgcn_s_sleep(1);
-        }
-    }
-    return __builtin_nanf("");
+    return await_state<SPLIT>(
+        ahead, kScanSpins,
+        [&](int j, uint32_t &state, uint64_t &map) {
+            const int64_t i = (at + j * step) * sp.width + col;
+            state = observe(sp.state + i);
+            map = ~(uint64_t)0;
+            if constexpr (SPLIT > 1) map = observe(sp.map + i);
+        },
+        [] { __builtin_amdgcn_s_sleep(1); });
 }
 
-// First slot of sequence n of a packed batch: it owns the slots from
-// floor(start / tile) + n on, as many as it has tiles, and at least one (a
-// sequence without tokens has its state handed on there).
 __device__ __forceinline__ int64_t scan_first_slot(const ScanParams &p, int n) {
-    int64_t base = p.cu[n];
-    base = base < 0 ? 0 : (base > p.total ? p.total : base);
-    return base / GDN_SCAN_TILE + n;
+    int64_t base, len;
+    clamp_sequence(p.cu[n], p.total, p.total, base, len);
+    return first_slot(base, n, GDN_SCAN_TILE);
 }
 
 // The sequence of a slot: the last one that starts at or before it, looked for

@@ -323,8 +323,10 @@ enum { GDN_SCAN_TILE = 128 };
  * from every other argument, contents ignored and overwritten). With at least
  * gdn_scan_workspace_size() bytes the call may cut the sequences along time
  * and run the pieces side by side; NULL or less runs each sequence's tiles one
- * after the other. Both give the same bits. Aliasing rules as for
- * gdn_prefill_chunked.
+ * after the other. Both give the same bits. Calls that may run at the same
+ * time need a workspace each: two that overlap on one neither hang nor leave
+ * their buffers, but their results are undefined (NaN, values left as they
+ * were, or finite wrong ones). Aliasing rules as for gdn_prefill_chunked.
  */
 gdn_status_t gdn_scan_prefill(const void *x, const void *alpha, const void *beta,
                               const float *initial_state, void *out, float *final_state,
