@@ -419,30 +419,40 @@ __global__ __launch_bounds__(256) void scan_decode_kernel(ScanDecodeParams p) {
     if (!bad && dst >= 0) store_raw(p.pool + (int64_t)dst * p.D, c0 * 4, pack<float>(h));
 }
 
-// Calls f with the kernel's element type, vector width and gate form as types:
-// 16-byte accesses where every row starts on 16 bytes.
+// Calls f with the kernel's element type, columns per thread and gate form as types.
 template <typename DT, int VEC, typename F>
 hipError_t with_scan_gates(bool tied, bool logits, F &&f) {
     if (tied)
         return logits ? f.template run<DT, VEC, true, true>() : f.template run<DT, VEC, true, false>();
     return logits ? f.template run<DT, VEC, false, true>() : f.template run<DT, VEC, false, false>();
 }
-// Columns per thread of the bf16 kernels. The backward one takes 4, in segments of
-// 128 bytes, where rows start on 64 bytes, and else pairs in segments of 256, of
-// which fewer straddle cache lines (4 x 4,097 x 2,056, both directions: 225 us
-// against 292; 2,080 189 in fours and 190).
+// Columns per thread, for the workspace's layout and the kernel alike: 16-byte
+// accesses where every row starts on 16 bytes, else pairs of bf16, else single
+// columns. The bf16 backward kernel takes 4, in segments of 128 bytes, where rows
+// start on 64 bytes, and else pairs in segments of 256, of which fewer straddle
+// cache lines (4 x 4,097 x 2,056, both directions: 232 us against 282; 2,080 189
+// in fours and 190).
+enum ScanPass { kForward, kBackward, kDecode };
 constexpr int kForVec = 8, kBackVec = 4, kBackRows = 32;
 
-template <int BVEC, typename F>
+int scan_vec(int32_t D, int dtype, ScanPass pass) {
+    if (dtype != 1) return D % 4 == 0 ? 4 : 1;
+    if (pass == kBackward ? D % kBackRows == 0 : D % kForVec == 0)
+        return pass == kBackward ? kBackVec : kForVec;
+    return D % 2 == 0 ? 2 : 1;
+}
+
+template <ScanPass PASS, typename F>
 hipError_t with_scan_types(int dtype, int32_t D, const void *b, uint32_t flags, F &&f) {
+    constexpr int kWide = PASS == kBackward ? kBackVec : kForVec;
     const bool tied = b == nullptr, logits = flags & GDN_GATE_LOGITS;
+    const int vec = scan_vec(D, dtype, PASS);
     if (dtype == 1)
-        return D % (BVEC == kBackVec ? kBackRows : BVEC) == 0
-                   ? with_scan_gates<__bf16, BVEC>(tied, logits, f)
-               : D % 2 == 0  ? with_scan_gates<__bf16, 2>(tied, logits, f)
-                             : with_scan_gates<__bf16, 1>(tied, logits, f);
-    return D % 4 == 0 ? with_scan_gates<float, 4>(tied, logits, f)
-                      : with_scan_gates<float, 1>(tied, logits, f);
+        return vec == kWide ? with_scan_gates<__bf16, kWide>(tied, logits, f)
+               : vec == 2   ? with_scan_gates<__bf16, 2>(tied, logits, f)
+                            : with_scan_gates<__bf16, 1>(tied, logits, f);
+    return vec == 4 ? with_scan_gates<float, 4>(tied, logits, f)
+                    : with_scan_gates<float, 1>(tied, logits, f);
 }
 
 template <typename DT, int VEC> int column_blocks(int32_t D) {
@@ -498,13 +508,15 @@ bool scan_wants_split(int64_t nseq, int64_t tokens, int64_t ncb, bool packed, in
     return nseq * ncb < 8 * (int64_t)cus || (packed && tokens >= nseq * GDN_SCAN_TILE);
 }
 
+// Channels of a tile.
 int scan_cols(int32_t D, int dtype, bool back) {
-    if (dtype == 1) {
-        if (back && D % kBackRows == 0) return ScanShape<__bf16, kBackVec>::kCols;
-        if (!back && D % kForVec == 0) return ScanShape<__bf16, kForVec>::kCols;
-        return D % 2 == 0 ? ScanShape<__bf16, 2>::kCols : ScanShape<__bf16, 1>::kCols;
-    }
-    return D % 4 == 0 ? ScanShape<float, 4>::kCols : ScanShape<float, 1>::kCols;
+    const int vec = scan_vec(D, dtype, back ? kBackward : kForward);
+    if (dtype == 1)
+        return vec == kForVec    ? ScanShape<__bf16, kForVec>::kCols
+               : vec == kBackVec ? ScanShape<__bf16, kBackVec>::kCols
+               : vec == 2        ? ScanShape<__bf16, 2>::kCols
+                                 : ScanShape<__bf16, 1>::kCols;
+    return vec == 4 ? ScanShape<float, 4>::kCols : ScanShape<float, 1>::kCols;
 }
 
 }  // namespace
@@ -613,7 +625,7 @@ hipError_t launch_scan(const ScanParams &p, int dtype, int cus, void *ws, size_t
     ScanSplit sp;
     const hipError_t e = prepare_split(p, dtype, cus, ws, ws_bytes, false, sp, stream);
     if (e != hipSuccess) return e;
-    return with_scan_types<kForVec>(dtype, p.D, p.b, p.flags, RunForward{p, sp, stream});
+    return with_scan_types<kForward>(dtype, p.D, p.b, p.flags, RunForward{p, sp, stream});
 }
 
 hipError_t launch_scan_backward(const ScanParams &p, int dtype, int cus, void *ws,
@@ -621,11 +633,11 @@ hipError_t launch_scan_backward(const ScanParams &p, int dtype, int cus, void *w
     ScanSplit sp;
     const hipError_t e = prepare_split(p, dtype, cus, ws, ws_bytes, true, sp, stream);
     if (e != hipSuccess) return e;
-    return with_scan_types<kBackVec>(dtype, p.D, p.b, p.flags, RunBackward{p, sp, stream});
+    return with_scan_types<kBackward>(dtype, p.D, p.b, p.flags, RunBackward{p, sp, stream});
 }
 
 hipError_t launch_scan_decode(const ScanDecodeParams &p, int dtype, hipStream_t stream) {
-    return with_scan_types<8>(dtype, p.D, p.b, p.flags, RunDecode{p, stream});
+    return with_scan_types<kDecode>(dtype, p.D, p.b, p.flags, RunDecode{p, stream});
 }
 
 }  // namespace gdn
