@@ -127,7 +127,7 @@ def _dtype_code(t: torch.Tensor) -> int:
         return GDN_BF16
     if t.dtype == torch.float32:
         return GDN_F32
-    raise TypeError(f"q, k, v must be bfloat16 or float32, got {t.dtype}")
+    raise TypeError(f"data tensors must be bfloat16 or float32, got {t.dtype}")
 
 
 _INT32 = 0x7FFFFFFF  # the library takes sizes in 32 bits; ctypes drops the bits above

@@ -286,3 +286,15 @@ def test_binding_refuses_what_32_bits_do_not_hold():
     with pytest.raises(ValueError, match="out of range"):
         g.gdn_varlen_prefill(q[0], q[0], q[0], ab[0], ab[0], cu, prefix_states=pre[:0].new_zeros(
             1, 1, 64, 64), prefix_interval=wrap + 1)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float64])
+def test_refused_types_are_named(dtype):
+    """By what they are, not by the mixer's arguments."""
+    import gated_deltanet_token_amd as g
+    x = torch.zeros(1, 4, 8, dtype=dtype)
+    for call in (lambda: g.gdn_scan_prefill(x, x, x), lambda: g.gdn_rms_norm(x, x[0, 0]),
+                 lambda: g.gdn_beam_select(x, torch.zeros(1, 4))):
+        with pytest.raises(TypeError, match=str(dtype)) as e:
+            call()
+        assert "q, k, v" not in str(e.value)
