@@ -300,8 +300,14 @@ size_t gdn_prefill_workspace_size(int32_t num_seqs, int64_t tokens, int32_t Hk,
  * alpha = exp(-softplus(a)) = sigmoid(-a), beta = sigmoid(b) (tied:
  * beta = sigmoid(a), formed without cancellation). Any other bit:
  * GDN_ERR_UNSUPPORTED. Unlike the delta-rule calls, alpha is used as given
- * (not clamped). 1 <= D <= 2^22; widths that are a multiple of 16 bytes run
- * on 16-byte accesses.
+ * (not clamped). 1 <= D <= 2^22.
+ *
+ * A NaN or infinity (in an input or a state) reaches no other channel or
+ * sequence and no earlier token; from its token on, out and the states of its
+ * channel are not finite, as the recurrence has it. Which of the two they are
+ * may differ from walking the tokens one by one: the product of the decays of
+ * a run of tokens may be 0 in fp32, and 0 times infinity is NaN. Gradients are
+ * the same towards earlier tokens.
  */
 
 /* Tokens per tile of the scan kernels: block starts at multiples of this are

@@ -518,3 +518,52 @@ def test_even_widths_elsewhere(gdn, tied):
     test_decode_slots(gdn, "bf16", 102, tied, 3)
     test_many_chains(gdn, (3, 385, 2046, "bf16", tied))
     test_many_chains(gdn, (2100, 130, 6, "bf16", tied))
+
+
+@gpu
+@pytest.mark.parametrize("T,D,dt", [(300, 72, "f32"), (300, 72, "bf16"), (700, 33, "f32")])
+@pytest.mark.parametrize("ws", ["auto", None])
+def test_infinities_stay_in_their_channel(gdn, T, D, dt, ws):
+    """An infinite state or input: what lies before it and beside it keeps its bits, what lies
+    behind it in its channel is not finite. Decays of 2^-10 (products of 0 over a tile)."""
+    B, dtype = 3, DT[dt]
+    x, a, b, s = inputs(T + D, B * T, D, B, dtype, False, False)
+    a[:, ::2] = 2.0 ** -10
+    a[a == 0] = 0.5  # 0 times infinity would be NaN token by token too
+    b[b == 0] = 0.5
+    dy = torch.randn(B * T, D, generator=torch.Generator().manual_seed(1)).to(dtype)
+    dh = torch.randn(B, D, generator=torch.Generator().manual_seed(2))
+    xd, ad, bd, sd, dyd, dhd = dev(x, a, b, s, dy, dh)
+    v = lambda t: t.view(B, T, D)  # noqa: E731
+    pre = torch.empty(B * (T // 128), D, device=DEV)
+    kw = dict(prefix_states=pre, prefix_interval=2, workspace=ws)
+    fwd = lambda: gdn.gdn_scan_prefill(v(xd), v(ad), v(bd), sd, **kw)  # noqa: E731
+    back = lambda: gdn.gdn_scan_backward(v(dyd), v(xd), v(ad), v(bd), sd, dfinal=dhd,  # noqa: E731
+                                         **kw)
+    out, fin = fwd()
+    grads = back()
+    inf = float("inf")
+    hit = torch.zeros(B, T, D, dtype=torch.bool)
+    sd[0, 4], sd[1, 5] = inf, -inf
+    v(xd)[2, 140, 6], v(xd)[2, T - 1, 7] = inf, -inf
+    hit[0, :, 4] = hit[1, :, 5] = True
+    hit[2, 140:, 6] = hit[2, T - 1:, 7] = True
+    o, f = fwd()
+    assert torch.equal(o.cpu()[~hit], out.cpu()[~hit]) and not o.cpu()[hit].isfinite().any()
+    last = hit[:, -1]
+    assert torch.equal(f.cpu()[~last], fin.cpu()[~last]) and not f.cpu()[last].isfinite().any()
+    # the gradients of clean inputs under an infinite gradient: from its token towards the first
+    sd.copy_(s)
+    xd.copy_(x)
+    fwd()
+    hit[:] = False
+    dhd[0, 4] = inf
+    v(dyd)[1, 140, 6] = -inf
+    hit[0, :, 4] = hit[1, :141, 6] = True
+    got = back()
+    for p, q in zip(got[:3], grads):
+        p, q = p.cpu(), q.cpu()
+        assert torch.equal(p[~hit], q[~hit]) and not p[hit].isfinite().any()
+    first = hit[:, 0]
+    p, q = got[3].cpu(), grads[3].cpu()
+    assert torch.equal(p[~first], q[~first]) and not p[first].isfinite().any()
