@@ -18,6 +18,11 @@ Beside the mixer: the gated linear recurrence with its gradients (gdn_scan_*),
 RMS norm with the residual's addition and an 8-bit output (gdn_rms_norm*),
 and beam search's selection over state slots (gdn_beam_select,
 gdn_gather_states).
+
+No call here records a graph for automatic differentiation: results carry no
+history, whatever requires_grad says of the inputs. To train through the norm
+or the scan, call the *_backward functions in the backward method of a
+torch.autograd.Function.
 """
 from __future__ import annotations
 
@@ -560,7 +565,8 @@ def gdn_scan_prefill(x, alpha, beta=None, initial_state=None, *, out=None, final
     (gdn_scan_backward takes them with an interval of 1 or 2). `stream` (a
     torch.cuda.Stream, here and in the calls below): where to run, the current
     one by default. It is for the caller to let it wait for the inputs; their
-    memory may be freed at once. Outputs made by the call belong to it."""
+    memory may be freed at once. Outputs made by the call belong to it. Results
+    have no autograd history: gdn_scan_backward gives the gradients."""
     return _scan_forward(x, alpha, beta, None, initial_state, out, final_state, want_final_state,
                          prefix_states, prefix_interval, flags, workspace)
 
@@ -708,7 +714,8 @@ def gdn_rms_norm(x, weight, residual=None, *, eps: float = 1e-6, group: int = 0,
     dtype. Returns (out, out8, scales, residual_out), None where not wanted:
     out8 is torch.float8_e4m3fn with fp32 scales, one per row (group 0, shape
     [..., 1]) or per 128 columns (group 128, [..., ceil(D / 128)]);
-    residual_out is x + residual (pass residual itself to update it in place)."""
+    residual_out is x + residual (pass residual itself to update it in place).
+    Results have no autograd history: gdn_rms_norm_backward gives the gradients."""
     lib = _lib or load_library()
     code, index, rows, D = _rows(x, "x")
     dt, shape = x.dtype, x.shape

@@ -330,3 +330,44 @@ def test_inputs_of_the_mixer_freed_after_a_call_on_another_stream(gdn):
     freed_after_the_call(lambda st, *t: gdn.gdn_decode_multi(*t, stream=st),
                          *[t[:, :3].contiguous() for t in (q, k, v, al, be)], r(B, Hv, D, D), ids,
                          ids)
+
+
+def test_autograd_through_a_function(gdn):
+    """Results carry no history by themselves, as documented; the backward calls inside a
+    torch.autograd.Function give every leaf the gradients that they give by hand."""
+    class Layer(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, res, w, a, b, h0):
+            y, _, _, r = gdn.gdn_rms_norm(x, w, res)
+            pre = torch.empty(gdn.prefix_state_rows(x.shape[0], x.shape[1], 2, False), x.shape[2],
+                              device=x.device)
+            h, hT = gdn.gdn_scan_prefill(y, a, b, h0, prefix_states=pre, prefix_interval=2,
+                                         flags=gdn.GDN_GATE_LOGITS)
+            ctx.save_for_backward(y, r, w, a, b, h0, pre)
+            return h, r, hT
+
+        @staticmethod
+        def backward(ctx, dh, dr, dhT):
+            y, r, w, a, b, h0, pre = ctx.saved_tensors
+            dy, da, db, dh0 = gdn.gdn_scan_backward(
+                dh.contiguous(), y, a, b, h0, prefix_states=pre, prefix_interval=2,
+                dfinal=dhT.contiguous(), flags=gdn.GDN_GATE_LOGITS)
+            dx, dw = gdn.gdn_rms_norm_backward(dy, r, w, dr.contiguous())
+            return dx, dx, dw.to(w.dtype), da, db, dh0
+
+    s = make(60)
+    leaves = [s[k].requires_grad_() for k in ("x", "res", "w", "a", "b", "h0")]
+    y, _, _, r = gdn.gdn_rms_norm(s["x"], s["w"], s["res"])
+    assert not (y.requires_grad or r.requires_grad)
+    h, r, hT = Layer.apply(*leaves)
+    (h.float().sum() + (r * s["dy"]).float().sum() + 2 * hT.sum()).backward()
+    with torch.no_grad():
+        y, _, _, r = gdn.gdn_rms_norm(s["x"], s["w"], s["res"])
+        gdn.gdn_scan_prefill(y, s["a"], s["b"], s["h0"], prefix_states=s["pre"], prefix_interval=2,
+                             flags=2)
+        dy, da, db, dh0 = gdn.gdn_scan_backward(
+            torch.ones_like(y), y, s["a"], s["b"], s["h0"], prefix_states=s["pre"],
+            prefix_interval=2, dfinal=torch.full_like(s["h0"], 2.0), flags=2)
+        dx, dw = gdn.gdn_rms_norm_backward(dy, r, s["w"], s["dy"])
+    for leaf, want in zip(leaves, (dx, dx, dw.bfloat16(), da, db, dh0)):
+        assert torch.equal(leaf.grad, want)
