@@ -19,7 +19,6 @@ namespace gdn {
 
 namespace {
 
-constexpr float kE4m3Max = 448.f;
 constexpr float kScaleFloor = 0x1p-100f;  // groups of zeros keep a finite scale and its inverse
 
 // 1 / sqrt(x) to about a unit in its last place: the instruction's value and one
@@ -37,27 +36,54 @@ __device__ __forceinline__ float row16_max(float x) {
     return x;
 }
 
-// x / d for values that share a d > 0, as x times the inverse in two terms: off by
-// less than 2^-45 beside the one rounding, so that a quotient halfway between two
-// e4m3 values comes out exactly and goes to the even one (the rounded inverse
-// alone lands on either side). An infinite d gives 0, and NaN of an infinite x.
-struct Divide {
-    float high, low;
-    __device__ __forceinline__ explicit Divide(float d) {
-        const float r = __builtin_amdgcn_rcpf(d);
-        const float e = fmaf(-d, r, 1.f);  // 1 / d = r (1 + e + e^2 + ...), |e| < 2^-22
-        high = r;
-        low = d < __builtin_inff() ? r * fmaf(e, e, e) : 0.f;
+// The scale of a group whose largest magnitude is `most`: most / 448, rounded once
+// (the product with the inverse in two terms, both positive for an infinity).
+__device__ __forceinline__ float e4m3_scale(float most) {
+    constexpr float high = (float)(1.0 / 448.0 - 0x1p-33), low = (float)(1.0 / 448.0 - (double)high);
+    static_assert(low >= 0.f, "inf - inf");
+    return fmaxf(fmaf(most, high, most * low), kScaleFloor);
+}
+
+// The row's s as a power of two times `rest`, in [4, 8) (NaN of a NaN).
+struct RowScale {
+    float pow2, rest;
+    __device__ __forceinline__ explicit RowScale(float s) {  // 2^-64 < s <= 2^63
+        const uint32_t top = __builtin_bit_cast(uint32_t, s) & 0x7F800000u;
+        pow2 = __builtin_bit_cast(float, top - (2u << 23));
+        rest = s * __builtin_bit_cast(float, (256u << 23) - top);
     }
-    __device__ __forceinline__ float operator()(float x) const { return fmaf(x, high, x * low); }
 };
 
-// The scale of a group whose largest magnitude is `most`: most / 448, rounded once.
-__device__ __forceinline__ float e4m3_scale(float most) {
-    constexpr float inv = 1.f / kE4m3Max;
-    const float q = most * inv;
-    return q < __builtin_inff() ? fmaxf(fmaf(fmaf(-q, kE4m3Max, most), inv, q), kScaleFloor) : q;
-}
+// y / scale of a group without y's roundings. With t = y / rest, the product of r,
+// a power of two and w, s cancels out and the quotient is 448 t / max |t|.
+// Products of bf16 are exact in t, their quotients are often halfway between two
+// e4m3 values (one in 10,000), and such a tie has to come out exactly to go to the
+// even one: the factor is kept in two terms, off by less than 2^-44 beside the one
+// rounding. (From the rounded y either side of a tie came out: 1,818 of 25 million
+// values of 196,608 x 128 bf16.) 448 / max |t| is a normal number in groups above
+// the smallest scale, t being at most a quarter of fp32's range where y is in it.
+struct E4m3Group {
+    float scale, high, low, rest;
+    __device__ __forceinline__ E4m3Group(float most, float s_rest) : rest(s_rest) {
+        scale = e4m3_scale(most * rest);
+        const float r = __builtin_amdgcn_rcpf(most);
+        high = 448.f * r;
+        low = fmaf(-most, high, 448.f) * r;
+        if (!(scale > kScaleFloor)) {  // the smallest scale: y over it
+            high = rest * (1.f / kScaleFloor);
+            low = 0.f;
+        }
+    }
+    __device__ __forceinline__ void quotients(float (&t)[8]) const {
+        if (scale < __builtin_inff()) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] = fmaf(t[e], high, t[e] * low);
+        } else {  // 0, and NaN of an infinite y
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] = t[e] * rest * 0.f;
+        }
+    }
+};
 
 struct SumOp {
     static __device__ __forceinline__ float row16(float x) { return row16_sum(x); }
@@ -212,9 +238,11 @@ template <typename DT, bool VEC, int TPR, int CH> struct NormRow {
 
 // Everything behind a row's loads. A row past the last one takes part with
 // zeros, for the lanes of a wave reduce together.
-template <typename DT, bool VEC, int TPR, int CH>
+// The weights of a thread's columns: `held` where it has them for several rows.
+template <typename DT, bool VEC, int TPR, int CH, bool HELD>
 __device__ __forceinline__ void norm_row(const NormParams &p, int64_t row, int tpr, int j,
-                                         float (&r)[CH][8], float (*s_red)[16]) {
+                                         float (&r)[CH][8], const float (&held)[HELD ? CH : 1][8],
+                                         float (*s_red)[16]) {
     const int D = p.D;
     const bool live = row < p.rows;
     const int64_t at = row * D;
@@ -229,16 +257,27 @@ __device__ __forceinline__ void norm_row(const NormParams &p, int64_t row, int t
     }
     ss = row_reduce<TPR, SumOp>(ss, s_red[0]);
     const float s = inv_sqrt(fmaf(ss, p.inv_d, p.eps));
+    const RowScale rs(s);
     float most = 0.f;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
         const int c = (k * tpr + j) * 8, left = live ? D - c : 0;
         if (left > 0) {
             float w[8];
-            load8<DT, VEC, false>(reinterpret_cast<const DT *>(p.w) + c, left, w);
+            if constexpr (HELD) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) r[k][e] = r[k][e] * s * w[e];
-            if (p.out) store8<DT, VEC, TPR == 0>(reinterpret_cast<DT *>(p.out) + at + c, left, r[k]);
+                for (int e = 0; e < 8; ++e) w[e] = held[k][e];
+            } else {
+                load8<DT, VEC, false>(reinterpret_cast<const DT *>(p.w) + c, left, w);
+            }
+            if (p.out) {
+                float y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = r[k][e] * s * w[e];
+                store8<DT, VEC, TPR == 0>(reinterpret_cast<DT *>(p.out) + at + c, left, y);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r[k][e] = r[k][e] * rs.pow2 * w[e];
         }
         if (!p.out8) continue;
         float m = 0.f;
@@ -247,26 +286,21 @@ __device__ __forceinline__ void norm_row(const NormParams &p, int64_t row, int t
         if (p.group == 0) {
             most = fmaxf(most, m);
         } else {  // 128 columns: the 16 lanes of a DPP row
-            m = e4m3_scale(row16_max(m));
-            const Divide over(m);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) r[k][e] = over(r[k][e]);
+            const E4m3Group g(row16_max(m), rs.rest);
+            g.quotients(r[k]);
             if (left > 0) {
                 store8_e4m3<VEC, TPR == 0>(p.out8 + at + c, left, r[k]);
-                if ((j & 15) == 0) p.scales[row * ((D + 127) / 128) + c / 128] = m;
+                if ((j & 15) == 0) p.scales[row * ((D + 127) / 128) + c / 128] = g.scale;
             }
         }
     }
     if (p.out8 && p.group == 0) {
-        most = row_reduce<TPR, MaxOp>(most, s_red[1]);
-        const float scale = e4m3_scale(most);
-        const Divide over(scale);
-        if (live && j == 0) p.scales[row] = scale;
+        const E4m3Group g(row_reduce<TPR, MaxOp>(most, s_red[1]), rs.rest);
+        if (live && j == 0) p.scales[row] = g.scale;
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
             const int c = (k * tpr + j) * 8, left = live ? D - c : 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) r[k][e] = over(r[k][e]);
+            g.quotients(r[k]);
             if (left > 0) store8_e4m3<VEC, TPR == 0>(p.out8 + at + c, left, r[k]);
         }
     }
@@ -287,9 +321,17 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p) {
 #pragma unroll
     for (int i = 0; i < NROWS; ++i)
         rows[i].load(p, row0 + i * per, row0 + i * per < p.rows, tpr, j);
+    constexpr bool HELD = NROWS > 1;
+    float w[HELD ? CH : 1][8];
+    if constexpr (HELD)
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            const int c = (k * tpr + j) * 8;
+            if (c < p.D) load8<DT, VEC, false>(reinterpret_cast<const DT *>(p.w) + c, p.D - c, w[k]);
+        }
 #pragma unroll
     for (int i = 0; i < NROWS; ++i)
-        norm_row<DT, VEC, TPR, CH>(p, row0 + i * per, tpr, j, rows[i].r, s_red);
+        norm_row<DT, VEC, TPR, CH, HELD>(p, row0 + i * per, tpr, j, rows[i].r, w, s_red);
 }
 
 // dx per row, and each workgroup's share of dw: a thread keeps the sums of its

@@ -447,8 +447,10 @@ size_t gdn_scan_workspace_size(int32_t num_seqs, int64_t tokens, int32_t D, gdn_
  *            for y. group 0: one scale per row (G = 1); group 128: one per 128
  *            columns (G = ceil(D / 128)); others: GDN_ERR_UNSUPPORTED.
  *
- * The sum, the mean and y are fp32; y is formed from the unrounded sum, and
- * out8 from the unrounded y. Sizes: rows >= 0, 1 <= D <= 16384, eps a
+ * The sum, the mean and y are fp32; y is formed from the unrounded sum. out8 is
+ * formed from r * weight, for the row's factor cancels in y / scale: where fp32
+ * holds those products (without a residual those of bf16), every value is the
+ * one of exact arithmetic, ties to even. Sizes: rows >= 0, 1 <= D <= 16384, eps a
  * normal fp32 number. At least one of out and out8. A NaN or Inf in a row, or
  * squares whose sum passes fp32's range, make NaN of that row.
  */
