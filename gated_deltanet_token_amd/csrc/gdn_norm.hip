@@ -262,8 +262,10 @@ __device__ __forceinline__ void norm_row(const NormParams &p, int64_t row, int t
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
         const int c = (k * tpr + j) * 8, left = live ? D - c : 0;
+        float w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = 0.f;
         if (left > 0) {
-            float w[8];
             if constexpr (HELD) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) w[e] = held[k][e];
@@ -276,10 +278,10 @@ __device__ __forceinline__ void norm_row(const NormParams &p, int64_t row, int t
                 for (int e = 0; e < 8; ++e) y[e] = r[k][e] * s * w[e];
                 store8<DT, VEC, TPR == 0>(reinterpret_cast<DT *>(p.out) + at + c, left, y);
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) r[k][e] = r[k][e] * rs.pow2 * w[e];
         }
         if (!p.out8) continue;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[k][e] = r[k][e] * rs.pow2 * w[e];
         float m = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(r[k][e]));
