@@ -15,8 +15,9 @@
 // waves, is a bound that at least W elements reach and few others do. They are
 // collected and ranked against each other by value and place, so that neither
 // ties nor the order of the collection change the result. Where too many reach
-// the bound (rows of equal values, or of hardly anything but -inf) W rounds
-// that each find the next best take its place.
+// the bound (rows of equal values, or of hardly anything but -inf), and in the
+// join where the candidates are more than its threads hold, W rounds that each
+// find the next best take its place.
 #include "gdn_device.hpp"
 #include "gdn_ops_launch.hpp"
 
@@ -88,11 +89,12 @@ __device__ __forceinline__ uint32_t wave_bound(uint32_t x, int want, int low) {
     return o;
 }
 
-// Logits per workgroup: VECS times 8 per thread. Bound by vector instructions,
-// above all the exponential of every logit (a quarter of the rate of a multiply):
-// 32 x 8 x 131,072 bf16 18 us, where its 67 MB would take 8 to 13. Eight waves
-// per SIMD cover the loads and the steps of a wave; the rounds read the logits
-// again so that they do not cost the registers for that.
+// Logits per workgroup: VECS times 8 per thread. Bound by vector instructions:
+// 32 x 8 x 131,072 bf16 18 us, where its 67 MB would take 8 to 13. A wave of 32
+// logits per lane has 389, 12 per logit, and its exponentials go at a quarter of
+// the rate: together they fill 13 us of the SIMDs. Eight waves per SIMD cover the
+// loads and the steps of a wave; the rounds read the logits again so that they do
+// not cost the registers for that.
 template <typename DT, int VECS>
 __global__ __launch_bounds__(kThreads, 8) void beam_piece_kernel(const DT *logits, int64_t V, int W,
                                                                  int npieces, uint32_t total,
@@ -310,9 +312,14 @@ __device__ __forceinline__ uint32_t score_bits(const Cand &c) {
 // One workgroup per batch item: the logsumexp of its beams, then the W best of
 // the pieces' candidates, found as in a piece (a bound from the scores rounded
 // down to 32 bits, then a ranking in fp64).
-// A thread holds up to HELD candidates; where there are more, all is done by
-// rounds. A chain of latencies: 5 us for one item of 4 beams and 16 pieces, 9 for
-// 32 items of 8 beams and 16 pieces.
+// A thread holds up to HELD candidates. A chain of latencies: 5 us for one item of
+// 4 beams and 16 pieces, 9 for 32 items of 8 beams and 16 pieces. Where W^2 pieces
+// are more than 8,192 all is done by rounds over them, by the one workgroup of the
+// item. One item: 9 beams from 206,849 to 229,376 tokens, 12 from 114,689 to
+// 172,032, 16 from 65,537 to 122,880 and from 262,145 on, 32 nearly always from
+// 16,385 on (pieces are 8,192 tokens long where that gives 256 workgroups, else
+// 2,048). A call takes 80 us for W = 9 and 220,000 tokens, where W = 8 takes 24 to
+// 29; 165 for 16 and 100,352; 390 for 32 and 32,000; 447 for 32 and 151,936.
 template <int THREADS, int HELD>
 __global__ __launch_bounds__(THREADS) void beam_join_kernel(BeamParams p, int npieces,
                                                             const PieceSum *sums,
@@ -442,7 +449,8 @@ __global__ __launch_bounds__(THREADS) void beam_join_kernel(BeamParams p, int np
 }
 
 // 16 KiB of one row per workgroup: a copy, 32 states of 3 MiB in 22.5 us (8.9 TB/s
-// read and written, parents that several beams share coming from cache).
+// read and written, parents that several beams share coming from cache). A short
+// row leaves most of its workgroup idle: 65,536 rows of 256 bytes 31 us (1.1 TB/s).
 __global__ __launch_bounds__(256) void gather_kernel(const u32x4 *src, int64_t num_src,
                                                      const int32_t *index, u32x4 *dst,
                                                      int64_t row_vecs, int parts, uint32_t total) {

@@ -9,9 +9,9 @@
 // once and held in registers between the sum of squares and the outputs.
 //
 // Mapping: a thread holds chunks of 8 neighbouring columns (16 bytes of bf16).
-// 16 threads share a row of up to 128 columns, a wave one of up to 512, and a
-// workgroup a wider one, so that a 128-column group is always 16 neighbouring
-// lanes and its maximum one DPP row reduction.
+// 16 threads share a row of up to 128 columns, a wave one of up to 512 (1,024 in
+// the backward pass), and a workgroup a wider one, so that a 128-column group is
+// always 16 neighbouring lanes and its maximum one DPP row reduction.
 #include "gdn_device.hpp"
 #include "gdn_ops_launch.hpp"
 
@@ -309,9 +309,10 @@ __device__ __forceinline__ void norm_row(const NormParams &p, int64_t row, int t
 }
 
 // NROWS rows per thread, their loads issued together. Bound by HBM for wide rows:
-// 16,384 x 5,120 bf16 with residual, to e4m3 and the new residual, 114 us (5.2
-// TB/s, a copy's rate); for rows of 128 by the row's own steps (196,608 rows 14
-// us from cache; 4 rows per thread 20, 1 row 17); 8 rows of 5,120 3.2 us.
+// 16,384 x 5,120 bf16 with residual, to e4m3 and the new residual, 115 us (5.1
+// TB/s, a copy's rate); by vector instructions for rows of 128: 196,608 rows 15
+// us, of which the 327 instructions of each of 24,576 waves fill 13 (4 rows per
+// thread took 20 us where 2 took 14 and 1 17); 8 rows of 5,120 3.4 us.
 template <typename DT, bool VEC, int TPR, int CH, int NROWS>
 __global__ __launch_bounds__(1024) void norm_kernel(NormParams p) {
     __shared__ float s_red[2][16];

@@ -59,10 +59,12 @@ __device__ __forceinline__ ScanTile take_tile(const ScanParams &p, const ScanSpl
 // (sequence, column block), its tiles in order: enough where that alone fills
 // the device, and without a workspace.
 //
-// Bound by HBM: 65,536 x 6,144 bf16 608 us (5.3 TB/s, the reads and writes
+// Bound by HBM: 65,536 x 6,144 bf16 610 us (5.3 TB/s, the reads and writes
 // counted at 1.01 times the tensors), 20,011 x 2,048 fp32 packed 130 us. Two
-// workgroups per CU (4 waves per SIMD) hold 196 KiB of loads in flight; gates
-// are formed once and kept with the products beta x as fp32.
+// workgroups of 512 threads per CU (4 waves per SIMD) hold 196 KiB of loads in
+// flight; those of 1,024 threads (pairs and single columns) share a CU up to 64
+// registers only, which the bf16 pairs pass with SPLIT 4 and 0 (79 and 94).
+// Gates are formed once and kept with the products beta x as fp32.
 template <typename DT, int VEC, bool TIED, bool LOGITS, int SPLIT>
 __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_forward_kernel(
     ScanParams p, int ncb, ScanSplit sp) {
@@ -184,11 +186,15 @@ __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads)) void scan_forward_k
 // in fp32 from the prefix state in front of it, so that no output is read and
 // the decay's gradient does not inherit a rounding of one.
 //
-// 7 elements of traffic per token and channel against some 60 vector
-// instructions, each of them counted: 4 x 4,097 x 2,048 bf16 100 us, 4.7 TB/s.
-// Registers decide: at most 128, for two workgroups per CU, so a thread holds 4
-// columns of bf16 (not 8: 143 us against 117 when that was chosen), the raw
-// words rather than their values, and one pair of columns' gradients at a time.
+// 7 elements of traffic per token and channel against 49 vector instructions
+// (780 per wave of 1,024 elements, which fill 43 us of the SIMDs): 4 x 4,097 x
+// 2,048 bf16 101 us, 4.7 TB/s. Registers decide: at most 128, for two workgroups
+// of 512 threads per CU, so a thread holds 4 columns of bf16 (not 8: 143 us
+// against 117 when that was chosen), the raw words rather than their values, and
+// one pair of columns' gradients at a time. The pairs and single columns of other
+// widths have 1,024 threads and, but for fp32 without SPLIT 4, more than 64
+// registers: one workgroup per CU, whose loads, chaining and gradients do not
+// overlap (4 x 4,097 x 2,056 148 to 158 us).
 template <typename DT, int VEC, bool TIED, bool LOGITS, int SPLIT>
 __global__ __launch_bounds__((ScanShape<DT, VEC>::kThreads), 4) void scan_backward_kernel(
     ScanParams p, int ncb, ScanSplit sp) {
@@ -479,7 +485,9 @@ struct ScanLayout {
 // How far the tiles of few chains look. The more tiles of a chain are under way
 // at once, the further back it pays to look, as long as the looking stays small:
 // with 4 chains (32,768 tokens of 512 bf16 channels) 4 deep takes 66 us and 1
-// deep 131, with 16 120 and 160, with 48 (65,536 x 6,144) 618 and 612.
+// deep 131, with 16 120 and 160, with 48 (65,536 x 6,144) 618 and 612. These are
+// long chains, most of whose tiles wait to be launched; short ones whose tiles
+// all run at once (2 x 1,000 x 1,111 has 36 of 8) follow the rule unmeasured.
 constexpr int kDeep = 4;
 constexpr int64_t kDeepChains = 24;
 

@@ -433,7 +433,8 @@ size_t gdn_scan_workspace_size(int32_t num_seqs, int64_t tokens, int32_t D, gdn_
 /*
  * gdn_rms_norm -- root-mean-square norm with the residual's addition and an
  * output in 8 bits with scales: the step in front of the mixer's projections
- * (with a residual) and behind the mixer per value head (rows of D = 128).
+ * (with a residual) and behind the mixer per value head (rows of D = 128; in 8
+ * bits where no output gate comes between the norm and the projection).
  *
  *   x        [rows, D] dtype
  *   residual [rows, D] dtype or NULL (none)
@@ -474,7 +475,7 @@ gdn_status_t gdn_rms_norm(const void *x, const void *residual, const void *weigh
  *   dx = s w dout - r s^3 mean(w dout r) + dresidual,
  *   dweight = sum over rows of dout r s (fp32, in a fixed order).
  * workspace: gdn_rms_norm_workspace_size(rows, D) bytes, required with dweight
- * (GDN_ERR_BAD_SHAPE when too small), unused without.
+ * (GDN_ERR_BAD_SHAPE when too small), unused without; for one call at a time.
  */
 gdn_status_t gdn_rms_norm_backward(const void *dout, const void *r, const void *weight,
                                    const void *dresidual, void *dx, float *dweight,
@@ -501,12 +502,13 @@ size_t gdn_rms_norm_workspace_size(int64_t rows, int32_t D);
  *            beam's source), or the index of gdn_gather_states
  *
  * A live beam w offers every token v at score_w + logit - logsumexp(logits_w),
- * compared in fp64; ties go to the lowest w * V + v. A beam whose score or
- * logsumexp is not finite (all logits -inf, any NaN or +inf) offers its tokens
- * at -inf, as does a logit of -inf. Sizes: B >= 1, 1 <= W <= 32, V >= 1,
+ * compared in fp64 (within a beam the W largest logits compete); ties go to the
+ * lowest w * V + v. A beam whose score or logsumexp is not finite (all logits
+ * -inf, any NaN or +inf) offers its tokens at -inf, as does a logit of -inf;
+ * finite logits of any size are masks or scores like others. Sizes: B >= 1, 1 <= W <= 32, V >= 1,
  * B * W * V < 2^40; eos in [0, V), or -1 for none (then finished and
  * new_finished are NULL). Results are the same from call to call.
- * workspace: gdn_beam_workspace_size() bytes, required.
+ * workspace: gdn_beam_workspace_size() bytes, required; for one call at a time.
  */
 gdn_status_t gdn_beam_select(const void *logits, const float *scores, const uint8_t *finished,
                              const int32_t *beam_slots, float *new_scores, int32_t *tokens,
