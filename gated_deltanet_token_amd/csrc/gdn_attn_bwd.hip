@@ -380,12 +380,26 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void attn_dkv_kernel(AttnBackwar
 // The same for bf16, with wave pairs that own 16 CT keys: the first of a pair forms p of tile
 // t (and dv), the second ds of tile t - 1 from the p that the first left in LDS (and dk).
 // One wave holds one set of owned rows and one of sums instead of two, so that two waves fit
-// a SIMD, one of each kind, whose exponentials and products overlap. p reaches ds as fp16
-// times 2^13 (half a step is 2^-11 of it, from 2^-27 on; as bf16, rounded once more as ds,
-// dk came out 2.9e-3 off and not 2.4e-3); the sums of both carry that factor until they are
-// stored. Three tiles in LDS: t - 1, t and the one under way.
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-constexpr float kPairLog2 = 13.f, kPairScale = 1.f / 8192.f;
+// a SIMD, one of each kind, whose exponentials and products overlap. Three tiles in LDS:
+// t - 1, t and the one under way.
+//
+// p lies in LDS in 16 bits (LDS holds no more at D = 128): of the fp32 value, whose sign is 0 and
+// whose highest exponent bit is 0 for anything below 2, the other 7 bits of the exponent and 9 of
+// the mantissa. Half a step is 2^-10 of p at any size that fp32 holds (rounded to bf16 there, and
+// once more as ds, dk came out 2.9e-3 off, relative to its norm, and not 2.4e-3; fp16 times 2^13
+// was as good for p above 2^-27 but nothing below 2^-38: keys that all queries nearly ignore lost
+// their dk; 2 x 4,097 tokens of 16/4 heads of 128, forward and backward: 737 us, so 726). p is at
+// most 1 but for the rounding of scores: larger ones count as just below 2.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t code_of(float p) {  // in the upper half
+    return (min(__builtin_bit_cast(uint32_t, p), 0x3FFFC000u) << 2) + 0x8000u;
+}
+__device__ __forceinline__ uint32_t code_pair(float p0, float p1) {
+    return __builtin_amdgcn_perm(code_of(p1), code_of(p0), 0x07060302u);
+}
+template <int I> __device__ __forceinline__ float code_value(uint32_t w) {
+    return __builtin_bit_cast(float, (uint32_t)__builtin_bit_cast(u16x2, w)[I] << 14);
+}
 template <typename DT, int D, int CT, int BQ> struct KeyPairs {
     using Tiles = KeyTiles<DT, D, CT, 8, BQ>;
     using A = Attend<DT, D, CT>;
@@ -492,30 +506,29 @@ template <typename DT, int D, int CT, int BQ> struct KeyPairs {
                     const bool cut = qs < w0 + CT * 16 || qs + 32 > len;
                     const int before_me = w0 + (lane & 15) - qs - 4 * g4;
                     const int left = len - qs - 4 * g4;
-                    f16x8 *const pp =
-                        reinterpret_cast<f16x8 *>(ps + sub / 32 * CT * 1024) + lane;
+                    u32x4 *const pp =
+                        reinterpret_cast<u32x4 *>(ps + sub / 32 * CT * 1024) + lane;
                     f32x4 st[2];
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
                         st[t] = *reinterpret_cast<const f32x4 *>(stat + sub + 16 * t + 4 * g4);
-                    if constexpr (!SECOND) {
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) st[t] = kPairLog2 - st[t];
-                    }
                     Frag<DT> f[CT];
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) {
-                        f16x8 h;
+                        u32x4 h;
                         if constexpr (SECOND) h = pp[ct * 64];
 #pragma unroll
                         for (int t = 0; t < 2; ++t)
 #pragma unroll
                             for (int r = 0; r < 4; ++r) {
                                 float w = sc[t][ct][r];
-                                if constexpr (SECOND)
-                                    w = (float)h[4 * t + r] * (w - st[t][r]);
-                                else
-                                    w = exp2_fast(fmaf(w, scale2, st[t][r]));
+                                if constexpr (SECOND) {
+                                    const uint32_t both = h[2 * t + r / 2];
+                                    w = (r & 1 ? code_value<1>(both) : code_value<0>(both)) *
+                                        (w - st[t][r]);
+                                } else {
+                                    w = exp2_fast(fmaf(w, scale2, -st[t][r]));
+                                }
                                 sc[t][ct][r] = w;
                             }
                         if (cut) {
@@ -529,7 +542,9 @@ template <typename DT, int D, int CT, int BQ> struct KeyPairs {
                         c_to_frag(sc[0][ct], sc[1][ct], f[ct]);
                         if constexpr (!SECOND) {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) h[i] = (_Float16)sc[i >> 2][ct][i & 3];
+                            for (int i = 0; i < 4; ++i)
+                                h[i] = code_pair(sc[i >> 1][ct][2 * (i & 1)],
+                                                 sc[i >> 1][ct][2 * (i & 1) + 1]);
                             pp[ct * 64] = h;
                         }
                     }
@@ -547,7 +562,7 @@ template <typename DT, int D, int CT, int BQ> struct KeyPairs {
             if (row >= len) continue;
             const int64_t at = (tok0 + row) * kvstride + kh * D + 4 * g4;
             const int64_t all = p.total * kvstride;
-            const float scale = SECOND ? p.scale * kPairScale : kPairScale;
+            const float scale = SECOND ? p.scale : 1.f;
             DT *to = static_cast<DT *>(SECOND ? p.dk : p.dv) + at;
             float *parts = p.parts + (2 * part + (SECOND ? 0 : 1)) * all + at;
 #pragma unroll
