@@ -43,7 +43,7 @@ gdn_status_t attn_forward(const PromptArgs &a, void *out, float *lse, hipStream_
 }
 
 size_t stats_bytes(const PromptArgs &a) {
-    return ((size_t)2 * a.Hq * a.tokens * 4 + 255) / 256 * 256;
+    return ((size_t)3 * a.Hq * a.tokens * 4 + 255) / 256 * 256;
 }
 int32_t head_split(const PromptArgs &a, int cus) {
     return gdn::attn_backward_split(a.n, a.longest, a.tokens, a.Hq, a.Hk, a.D, code(a.dtype),

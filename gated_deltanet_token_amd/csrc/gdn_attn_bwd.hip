@@ -7,6 +7,12 @@
 //   dv_j = sum_t p_tj dout_t,   dk_j = scale sum_t ds_tj q_t
 // dk and dv sum over the query heads of the key head as well.
 //
+// lse is held in fp32, so a weight formed from it is off by up to 3 2^-24 |lse| (seen: 9 % at
+// scores of 2^20, whose differences fp32 still holds, and a factor of 2 at 2^23). A row's weights
+// share that factor. The dq kernel, which forms all of a row's weights, sums them, divides
+// its row by the sum and leaves 1 / sum for the weights in dk and dv (4 x 2,048 tokens of 16/4
+// heads of 64, forward and backward: 261 us, 258 without; 128 and 256 wide as fast).
+//
 // Three kernels: the rows' statistics; dq by query tiles (three products per pair
 // of tiles); dk and dv by key tiles (four). Scores and dout . v are formed in both:
 // 7 products where 5 would do, but every sum has one owner, so that no atomics and
@@ -25,7 +31,8 @@ namespace gdn {
 
 namespace {
 
-// log2-scaled lse and delta of every (head, token). 16 lanes per row of D.
+// log2-scaled lse and delta of every (head, token), the first two of p.stats. 16 lanes per row
+// of D.
 template <typename DT, int D>
 __global__ __launch_bounds__(256) void attn_stats_kernel(AttnBackwardParams p) {
     const int64_t rows = p.total * p.Hq;
@@ -97,18 +104,19 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void attn_dq_kernel(AttnBackward
     const int q0 = tile * BM, w0 = q0 + wave * CT * 16, kh = head / (p.Hq / p.Hk);
 
     Frag<DT> qf[D / 32][CT], df[D / 32][CT];
-    float lse[CT], delta[CT];
-    int lim[CT];
+    float lse[CT], delta[CT], sum[CT];  // sum: of the weights, the lane's own part of them
+    // keys that the lane's query sees
+    auto sees = [&](int ct) { return min(w0 + 16 * ct + (fresh(lane) & 15), len - 1) + 1; };
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
         const int row = min(w0 + 16 * ct + c, len - 1);
-        lim[ct] = row + 1;
         const int64_t at = ((tok0 + row) * p.Hq + head) * D;
 #pragma unroll
         for (int kk = 0; kk < D / 32; ++kk) {
             qf[kk][ct] = R::load(static_cast<const DT *>(p.q) + at, kk, g4);
             df[kk][ct] = R::load(static_cast<const DT *>(p.dout) + at, kk, g4);
         }
+        sum[ct] = 0.f;
         lse[ct] = p.stats[(int64_t)head * p.total + tok0 + row];
         delta[ct] = p.stats[((int64_t)p.Hq + head) * p.total + tok0 + row];
     }
@@ -140,7 +148,7 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void attn_dq_kernel(AttnBackward
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
                 bool nan = false;
-                for (int row = 0; row < BK; ++row) nan |= odd[row] && key + row < lim[ct];
+                for (int row = 0; row < BK; ++row) nan |= odd[row] && key + row < sees(ct);
                 if (nan) lse[ct] = __builtin_nanf("");
             }
             __syncthreads();
@@ -150,22 +158,28 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void attn_dq_kernel(AttnBackward
         if (sizeof(DT) == 2 && key == 0 && w0 < 32) {
             // The first 32 queries see few keys, and dout . v_j - delta is a small difference
             // of large terms where one key has most of the weight: from out as stored (off by
-            // up to 2^-9) the gradients of two-token sequences came out up to 2e-2 off, relative
+            // up to 2^-8) the gradients of two-token sequences came out up to 2e-2 off, relative
             // to their norm. delta is also sum_j p_tj (dout_t . v_j), here over one tile.
             f32x4 sc[2][CT], dp[2][CT];
             A::scores(kt, 0, qf, sc, lane);
             A::scores(vt, 0, df, dp, lane);
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
-                float sum = 0.f;
+                const int lim = sees(ct);
+                float all = 0.f, of = 0.f;
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const float w = exp2_fast(fmaf(sc[t][ct][r], scale2, -lse[ct]));
-                        if (16 * t + 4 * g4 + r < lim[ct]) sum = fmaf(w, dp[t][ct][r], sum);
+                        if (16 * t + 4 * g4 + r < lim) {
+                            all += w;
+                            of = fmaf(w, dp[t][ct][r], of);
+                        }
                     }
-                delta[ct] = across_sum(sum);
+                all = across_sum(all);
+                of = across_sum(of);
+                delta[ct] = all == 0.f ? of : of / all;
                 const int row = w0 + 16 * ct + c;
                 if (g4 == 0 && row < len)  // for dk and dv
                     p.stats[((int64_t)p.Hq + head) * p.total + tok0 + row] = delta[ct];
@@ -182,19 +196,23 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void attn_dq_kernel(AttnBackward
             const bool cut = k + 32 > w0 + 1;
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
+                if (cut) {
+                    const int lim = sees(ct);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (k + 16 * (i >> 2) + 4 * g4 + (i & 3) >= lim) {
+                            sc[i >> 2][ct][i & 3] = -__builtin_inff();
+                            dp[i >> 2][ct][i & 3] = 0.f;
+                        }
+                }
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const float w = exp2_fast(fmaf(sc[t][ct][r], scale2, -lse[ct]));
+                        sum[ct] += w;
                         dp[t][ct][r] = w * (dp[t][ct][r] - delta[ct]);
                     }
-                if (cut) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (k + 16 * (i >> 2) + 4 * g4 + (i & 3) >= lim[ct])
-                            dp[i >> 2][ct][i & 3] = 0.f;
-                }
                 c_to_frag(dp[0][ct], dp[1][ct], f[ct]);
             }
             A::add_to(acc, kt, sub, f, lane);
@@ -203,10 +221,14 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void attn_dq_kernel(AttnBackward
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
         const int row = w0 + 16 * ct + c;
+        const float all = across_sum(sum[ct]);
         if (row >= len) continue;
+        // no weights at all, or NaN: as they are
+        const float f = all > 0.f ? 1.f / all : 1.f;
         DT *o = static_cast<DT *>(p.dq) + ((tok0 + row) * p.Hq + head) * D + 4 * g4;
 #pragma unroll
-        for (int dt = 0; dt < D / 16; ++dt) store4(o + 16 * dt, acc[dt][ct] * p.scale);
+        for (int dt = 0; dt < D / 16; ++dt) store4(o + 16 * dt, acc[dt][ct] * (p.scale * f));
+        if (g4 == 0) p.stats[((int64_t)2 * p.Hq + head) * p.total + tok0 + row] = f;
     }
 }
 
@@ -227,7 +249,7 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void attn_dkv_kernel(AttnBackwar
     using A = Attend<DT, D, CT>;
     using R = Rows<DT, D>;
     constexpr int BN = NW * CT * 16, kTile = Tiles::kTile;
-    constexpr int kBuf = 2 * kTile + 512;  // queries, dout, 64 lse, 64 delta
+    constexpr int kBuf = 2 * kTile + 768;  // queries, dout, 64 lse, 64 delta, 64 factors
     extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
     __shared__ int odd[BQ];
     const int lane = threadIdx.x & 63, c = lane & 15, g4 = lane >> 4;
@@ -273,7 +295,7 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void attn_dkv_kernel(AttnBackwar
             static_cast<const unsigned char *>(p.dout) + tok0 * stride + j * R::kPitch, stride,
             len};
         Tiles::issue(src, q, (uint32_t)stride, buf, wave, lane);
-        if (wave < 2) {
+        if (wave < 3) {
             const float *st = p.stats + ((int64_t)wave * p.Hq + j) * p.total + tok0 + q;
             dma4_async(uniform(reinterpret_cast<const unsigned char *>(st)),
                        (uint32_t)min(lane, len - 1 - q) * 4, buf + 2 * kTile + wave * 256);
@@ -287,7 +309,7 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void attn_dkv_kernel(AttnBackwar
             __syncthreads();
             unsigned char *buf = lds + parity * kBuf, *qt = buf, *dt_ = buf + kTile;
             const float *lse = reinterpret_cast<const float *>(buf + 2 * kTile);
-            const float *delta = lse + 64;
+            const float *delta = lse + 64, *factor = lse + 128;
             const bool wrap = q + BQ >= len;
             if (!wrap || j + 1 < j1)
                 issue(wrap ? j + 1 : j, wrap ? first : q + BQ, lds + (parity ^ 1) * kBuf);
@@ -319,12 +341,14 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void attn_dkv_kernel(AttnBackwar
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     const f32x4 ls = *reinterpret_cast<const f32x4 *>(lse + sub + 16 * t + 4 * g4);
+                    const f32x4 fa =
+                        *reinterpret_cast<const f32x4 *>(factor + sub + 16 * t + 4 * g4);
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
                             const int row = qs + 16 * t + 4 * g4 + r;
-                            float w = exp2_fast(fmaf(sc[t][ct][r], scale2, -ls[r]));
+                            float w = exp2_fast(fmaf(sc[t][ct][r], scale2, -ls[r])) * fa[r];
                             if (cut && (row < own[ct] || row >= len)) w = 0.f;
                             sc[t][ct][r] = w;
                         }
@@ -388,8 +412,8 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void attn_dkv_kernel(AttnBackwar
 // the mantissa. Half a step is 2^-10 of p at any size that fp32 holds (rounded to bf16 there, and
 // once more as ds, dk came out 2.9e-3 off, relative to its norm, and not 2.4e-3; fp16 times 2^13
 // was as good for p above 2^-27 but nothing below 2^-38: keys that all queries nearly ignore lost
-// their dk; 2 x 4,097 tokens of 16/4 heads of 128, forward and backward: 737 us, so 726). p is at
-// most 1 but for the rounding of scores: larger ones count as just below 2.
+// their dk; 2 x 4,097 tokens of 16/4 heads of 128, forward and backward: 728 us, so 720). p is at
+// most 1, its row's sum being 1; should it not be, it counts as just below 2.
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t code_of(float p) {  // in the upper half
     return (min(__builtin_bit_cast(uint32_t, p), 0x3FFFC000u) << 2) + 0x8000u;
@@ -405,7 +429,7 @@ template <typename DT, int D, int CT, int BQ> struct KeyPairs {
     using A = Attend<DT, D, CT>;
     using R = Rows<DT, D>;
     static constexpr int kRows = 4 * CT * 16, kTile = Tiles::kTile;
-    static constexpr int kBuf = 2 * kTile + 512;    // queries, dout, 64 lse, 64 delta
+    static constexpr int kBuf = 2 * kTile + 768;  // queries, dout, 64 lse, 64 delta, 64 factors
     static constexpr int kP = BQ / 32 * CT * 1024;  // p of a pair and tile
     static constexpr int kLds = 3 * kBuf + 8 * kP;
 
@@ -444,7 +468,7 @@ template <typename DT, int D, int CT, int BQ> struct KeyPairs {
                 static_cast<const unsigned char *>(p.dout) + tok0 * stride + j * R::kPitch,
                 stride, len};
             Tiles::issue(src, q, (uint32_t)stride, buf, wave, lane);
-            if (wave < 2) {
+            if (wave < 3) {
                 const float *st = p.stats + ((int64_t)wave * p.Hq + j) * p.total + tok0 + q;
                 dma4_async(uniform(reinterpret_cast<const unsigned char *>(st)),
                            (uint32_t)min(lane, len - 1 - q) * 4, buf + 2 * kTile + wave * 256);
@@ -508,29 +532,34 @@ template <typename DT, int D, int CT, int BQ> struct KeyPairs {
                     const int left = len - qs - 4 * g4;
                     u32x4 *const pp =
                         reinterpret_cast<u32x4 *>(ps + sub / 32 * CT * 1024) + lane;
-                    f32x4 st[2];
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        st[t] = *reinterpret_cast<const f32x4 *>(stat + sub + 16 * t + 4 * g4);
+                    for (int t = 0; t < 2; ++t) {
+                        const float *of = stat + sub + 16 * t + 4 * g4;
+                        const f32x4 st = *reinterpret_cast<const f32x4 *>(of);
+                        f32x4 fa;
+                        if constexpr (!SECOND) fa = *reinterpret_cast<const f32x4 *>(of + 128);
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const float w = sc[t][ct][r];
+                                if constexpr (SECOND)
+                                    sc[t][ct][r] = w - st[r];
+                                else
+                                    sc[t][ct][r] = exp2_fast(fmaf(w, scale2, -st[r])) * fa[r];
+                            }
+                    }
                     Frag<DT> f[CT];
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) {
                         u32x4 h;
                         if constexpr (SECOND) h = pp[ct * 64];
+                        if constexpr (SECOND) {
 #pragma unroll
-                        for (int t = 0; t < 2; ++t)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                float w = sc[t][ct][r];
-                                if constexpr (SECOND) {
-                                    const uint32_t both = h[2 * t + r / 2];
-                                    w = (r & 1 ? code_value<1>(both) : code_value<0>(both)) *
-                                        (w - st[t][r]);
-                                } else {
-                                    w = exp2_fast(fmaf(w, scale2, -st[t][r]));
-                                }
-                                sc[t][ct][r] = w;
-                            }
+                            for (int i = 0; i < 8; ++i)
+                                sc[i >> 2][ct][i & 3] *=
+                                    i & 1 ? code_value<1>(h[i / 2]) : code_value<0>(h[i / 2]);
+                        }
                         if (cut) {
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
@@ -655,7 +684,7 @@ hipError_t launch(const AttnBackwardParams &p, int cus, hipStream_t stream) {
     if (e != hipSuccess) return e;
     const HeadOrder o = order((int64_t)p.Hk * p.split, S::kBN);
     if constexpr (S::kWide) {
-        constexpr int kLds = KeyTiles<DT, D, S::kKCT, 4, S::kKBQ>::kLds + 2 * 512;
+        constexpr int kLds = KeyTiles<DT, D, S::kKCT, 4, S::kKBQ>::kLds + 2 * 768;
         const auto kernel = attn_dkv_kernel<DT, D, S::kKCT, 4, S::kKBQ, S::kKPer>;
         if ((e = with_lds(kernel, kLds)) != hipSuccess) return e;
         kernel<<<grid_of(o.grid(), 256), 256, kLds, stream>>>(p, o);

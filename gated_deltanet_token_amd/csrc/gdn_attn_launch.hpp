@@ -28,7 +28,7 @@ struct AttnBackwardParams {
     int64_t T, total;
     int32_t N, Hq, Hk;
     float scale;
-    float *stats;   // workspace: [2][Hq][total], log2-scaled lse and delta
+    float *stats;   // workspace: [3][Hq][total], log2-scaled lse, delta, 1 / sum of weights
     float *parts;   // workspace: [split][2][total][Hk][D] partial dk, dv (split > 1)
     int32_t split;  // workgroups that share the query heads of a key head
 };

@@ -547,7 +547,7 @@ gdn_status_t gdn_gather_states(const void *src, int64_t num_src, const int32_t *
  * are all -infinity counts as one. An infinity or NaN in a key or value that a
  * query does not see (a later token, another sequence, the rest of a page)
  * does not reach it; what it reaches is not finite. Scores (scale q . k) beyond
- * 2^28 in magnitude (2^24 in the gradients) may give NaN.
+ * 2^28 in magnitude may give NaN.
  */
 
 /*
