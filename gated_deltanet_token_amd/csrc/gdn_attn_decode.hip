@@ -356,11 +356,8 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_few_kernel(DecodePlan d) {
 #pragma unroll
             for (int x = 0; x < NW; ++x) {
                 const float mx = ml[x][0][row];
-                if (mx == -__builtin_inff()) {  // no key seen (or its sums are NaN: l tells)
-                    l += ml[x][1][row];
-                    continue;
-                }
-                const float f = exp2_fast(mx - m);
+                // no key seen, or scores of -inf alone: sums of 0, or NaN
+                const float f = mx == -__builtin_inff() ? 1.f : exp2_fast(mx - m);
                 l += ml[x][1][row] * f;
                 const float *from = reinterpret_cast<const float *>(lds + x * kRing);
                 a += *reinterpret_cast<const f32x4 *>(from + place(row, dd)) * f;

@@ -1,6 +1,7 @@
-"""Weights at the ends of their range in causal attention and its gradients: scores so large that
-fp32 holds them in steps of a quarter, weights so small that 16 bits lose them. Scores are sums of
-integers below 2^24 and exact in fp32 in any order, so the bounds here hold no error of theirs."""
+"""Weights at the ends of their range in attention and its gradients: scores so large that fp32
+holds them in steps of a quarter, weights so small that 16 bits lose them, weights of 0. Scores
+are sums of integers below 2^24 and exact in fp32 in any order, so the bounds of the tests of large
+ones hold no error of theirs."""
 import math
 
 import pytest
@@ -187,3 +188,28 @@ def test_gradients_of_short_sequences_as_a_whole(gdn, D):
             zip(*[backward64(do[i], q[i], k[i], v[i], torch.bfloat16)[0] for i in range(N)])]
     for x, w, name in zip(got, want, ("dq", "dk", "dv")):
         assert off(x, w) < 4e-3, name
+
+
+# ---------------------------------------------------------------- weights of 0
+
+
+def test_a_value_that_is_not_finite_behind_infinite_keys(gdn):
+    """A tile of keys whose scores are all -infinity (keys of infinity against a negative query)
+    beside a tile of ordinary ones, dealt to another wave or the same: a NaN among the tile's
+    values is seen and reaches its column of out, as it does over whole prompts."""
+    D, page, n = 64, 32, 96
+    for tile in (0, 1, 2):
+        q = torch.full((1, 1, 1, D), -1.0)
+        k = torch.randn(n, 1, D, generator=torch.Generator().manual_seed(tile))
+        v = torch.randn(n, 1, D, generator=torch.Generator().manual_seed(tile + 9))
+        k[32 * tile:32 * tile + 32, 0, 3] = float("inf")
+        v[32 * tile + 5, 0, 7] = float("nan")
+        for dtype in (torch.bfloat16, torch.float32):
+            kc, vc = (x.view(n // page, page, 1, D).to(dtype).to(DEV) for x in (k, v))
+            table = torch.arange(n // page, dtype=torch.int32, device=DEV)[None]
+            out, _ = gdn.gdn_attn_decode(q.to(dtype).to(DEV), kc, vc, table,
+                                         torch.tensor([n], dtype=torch.int32, device=DEV))
+            lost = torch.zeros(D, dtype=torch.bool)
+            lost[7] = True
+            out = out[0, 0, 0].cpu()
+            assert torch.isnan(out[lost]).all() and torch.isfinite(out[~lost]).all(), (tile, dtype)
