@@ -308,7 +308,12 @@ template <typename DT, int D, int CT, bool FRESH = kFresh<DT, D>> struct Attend 
         }
     }
 
-    // Settled scores to weights; p as the B operands of the next product.
+    // Settled scores to weights; p as the B operands of the next product, rounded to the
+    // tensors' type: off by half a step of each weight, which is sqrt(2) times the error of
+    // rounding the result alone (bf16: 2.3e-3 of its norm and not 1.7e-3). The rest as a second
+    // term (below) is not worth its products where these are what bounds: 8,192 tokens of 24/4
+    // heads of 256 808 us, so 1,057; 2 x 8,192 of 16/4 heads of 128 525 and 710; 64 sequences
+    // behind 32,768 shared tokens 113 and 126.
     template <int NT>
     __device__ __forceinline__ void weights(f32x4 (&s)[NT][CT], Frag<DT> (&p)[NT / 2][CT],
                                             float c) {
@@ -327,6 +332,19 @@ template <typename DT, int D, int CT, bool FRESH = kFresh<DT, D>> struct Attend 
         }
     }
 
+    // What the weights of 32 keys lose as operands in bf16, as operands too (together off by
+    // 2^-17 at the most).
+    static __device__ __forceinline__ void rest(const f32x4 (&s)[2][CT], const Frag<DT> (&p)[CT],
+                                                Frag<DT> (&low)[CT]) {
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            f32x4 d[2];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d[i >> 2][i & 3] = s[i >> 2][ct][i & 3] - to_f32(p[ct][i]);
+            c_to_frag(d[0], d[1], low[ct]);
+        }
+    }
+
     // acc += p v over the 32 keys.
     template <int DEPTH = FRESH ? 1 : 0>
     __device__ __forceinline__ void add(const unsigned char *vt, int r0, const Frag<DT> (&p)[CT],
@@ -337,6 +355,14 @@ template <typename DT, int D, int CT, bool FRESH = kFresh<DT, D>> struct Attend 
     static __device__ __forceinline__ void add_to(f32x4 (&acc)[D / 16][CT],
                                                   const unsigned char *vt, int r0,
                                                   const Frag<DT> (&p)[CT], int lane) {
+        const Frag<DT> *const terms[1] = {p};
+        add_terms<DEPTH>(acc, vt, r0, terms, lane);
+    }
+    // acc += (p_0 + .. + p_(N-1)) v.
+    template <int DEPTH = FRESH ? 1 : 0, int N>
+    static __device__ __forceinline__ void add_terms(f32x4 (&acc)[D / 16][CT],
+                                                     const unsigned char *vt, int r0,
+                                                     const Frag<DT> *const (&p)[N], int lane) {
         lane = fresh<FRESH>(lane);
         const int c = lane & 15, g4 = lane >> 4;
         constexpr int kStep = 2;  // columns of 16 per step
@@ -355,9 +381,11 @@ template <typename DT, int D, int CT, bool FRESH = kFresh<DT, D>> struct Attend 
 #pragma unroll
             for (int j = 0; j < kStep; ++j)
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-                    acc[kStep * i + j][ct] =
-                        mma(a[i % (DEPTH + 1)][j], p[ct], acc[kStep * i + j][ct]);
+                for (int n = 0; n < N; ++n)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+                        acc[kStep * i + j][ct] =
+                            mma(a[i % (DEPTH + 1)][j], p[n][ct], acc[kStep * i + j][ct]);
             if constexpr (DEPTH > 0) in_order();
         }
     }

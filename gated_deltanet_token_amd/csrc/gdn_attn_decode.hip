@@ -12,7 +12,9 @@
 // to the workgroups in equal runs, whatever the lengths; the waves of a workgroup
 // stream tiles of their own through LDS of their own, no barrier between them, so
 // that every wave always has a tile of keys or of values under way. 64 sequences of up
-// to 16,384 tokens, 24/4 heads of 256, with the join: 102 us, 5.1 TB/s.
+// to 16,384 tokens, 24/4 heads of 256, with the join: 102 us, 5.1 TB/s. The matrix instructions
+// have time to spare: bf16 weights are two terms, rounded and rest, so that nothing but the result
+// is rounded (102 us either way; with 4 new tokens each, 24 rows, 128 us, in one term 125).
 //
 // attn_rows_kernel: many query rows against one run of keys: the rows of all
 // sequences of a group against their prefix (read once for all of them), or
@@ -271,7 +273,7 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_few_kernel(DecodePlan d) {
                     for (int half = 0; half < 2; ++half) next[half] = half_of(t + NW, half);
                 }
                 f32x4 s[2][CT];
-                Frag<DT> w[1][CT];
+                Frag<DT> w[1][CT], low[CT];
                 wait_copies<kCopies>();  // the keys; the values are still under way
                 st.scores(kt, 0, qf, s, lane);
                 if (more) {
@@ -295,6 +297,7 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_few_kernel(DecodePlan d) {
                 if (cut) st.mask(s, seen, lane);
                 st.settle(s, scale2);
                 st.weights(s, w, scale2);
+                if constexpr (sizeof(DT) == 2) st.rest(s, w[0], low);
                 if (more)
                     wait_copies<kCopies>();
                 else
@@ -311,7 +314,12 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_few_kernel(DecodePlan d) {
                         }
                     }
                 }
-                st.add(vt, 0, w[0], lane);
+                if constexpr (sizeof(DT) == 2) {
+                    const Frag<DT> *const terms[2] = {w[0], low};
+                    st.add_terms(st.acc, vt, 0, terms, lane);
+                } else {
+                    st.add(vt, 0, w[0], lane);
+                }
                 if (more) {
                     __builtin_amdgcn_s_waitcnt(0xC07F);  // the values have been read
 #pragma unroll

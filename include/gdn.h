@@ -540,8 +540,10 @@ gdn_status_t gdn_gather_states(const void *src, int64_t num_src, const int32_t *
  * head i / (Hq / Hk). q, k, v, out, the caches and the gradients have the
  * element type `dtype`; sums, softmax statistics and lse are fp32; in bf16 the
  * weights (and the gradients' inner terms) are rounded to bf16 as operands of
- * the matrix products. Hq a multiple of Hk, D in {64, 128, 256}, Hq * D <= 2^24,
- * scale positive and finite (1 / sqrt(D) as a rule).
+ * the matrix products (not so in gdn_attn_decode for a sequence's own tokens
+ * where K Hq / Hk <= 32: there they are two bf16 terms). Hq a multiple of Hk, D
+ * in {64, 128, 256}, Hq * D <= 2^24, scale positive and finite (1 / sqrt(D) as a
+ * rule).
  *
  * A query without any key has out = 0 and lse = -infinity; one whose scores
  * are all -infinity counts as one. An infinity or NaN in a key or value that a
