@@ -922,7 +922,9 @@ def _prompt(q, k, v, cu, name="q", first=None):
 
 
 def _scale(scale, D):
-    return D ** -0.5 if scale is None else float(scale)
+    if scale is None:
+        return D ** -0.5 if D > 0 else 1.0  # heads of no columns are refused by the library
+    return float(scale)
 
 
 def _attn_forward(q, k, v, cu, scale, out, lse, want_lse):
