@@ -146,9 +146,11 @@ const char *gdn_status_string(gdn_status_t s) {
     case GDN_ERR_NULL_POINTER: return "a required pointer is NULL";
     case GDN_ERR_BAD_SHAPE: return "a size is out of range or inconsistent";
     case GDN_ERR_UNSUPPORTED:
-        return "unsupported dtype, flag or head dimension (Dk == Dv in {64, 128}), a shape whose "
-               "scratch exceeds the static 64 MiB of gdn_prefill_chunked_noalloc, or a width, "
-               "group, interval or beam count the library has no kernel for";
+        return "unsupported dtype, flag or head dimension (mixer: Dk == Dv in {64, 128}; attention: "
+               "64, 128 or 256; rotary: a multiple of 8 up to 1024), a page size that is no power "
+               "of two from 16 to 2^20, a shape whose scratch exceeds the static 64 MiB of "
+               "gdn_prefill_chunked_noalloc, or a width, group, interval or beam count the "
+               "library has no kernel for";
     case GDN_ERR_MISALIGNED: return "a pointer is not 16-byte aligned (index arrays: 4-byte)";
     case GDN_ERR_ALIAS: return "forbidden overlap between buffers";
     case GDN_ERR_HIP: return g_detail[0] ? g_detail : "HIP runtime error";

@@ -26,3 +26,10 @@ def test_heads_of_no_columns(gdn):
                  lambda: gdn.gdn_attn_decode(q, cache, cache, table, lengths)):
         with pytest.raises(gdn.GDNError, match="size is out of range"):
             call()
+
+
+def test_message_of_an_unsupported_call(gdn):
+    """Whoever passes heads of 96 columns, or pages of 24 tokens, reads what there is."""
+    text = gdn.load_library().gdn_status_string(3).decode()
+    assert "attention: 64, 128 or 256" in text and "page size" in text
+    assert str(gdn.GDNError(3, text)).endswith(text)
