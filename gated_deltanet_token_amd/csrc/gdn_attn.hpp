@@ -128,9 +128,6 @@ template <typename DT, int D> struct Rows {
         }
         return f;
     }
-    static __device__ __forceinline__ float get(const unsigned char *t, int row, int d) {
-        return to_f32(*reinterpret_cast<const DT *>(t + at(row, d)));
-    }
     // Natural fragment of a row in global memory (elements 32 kk + 8 g4 + e).
     static __device__ __forceinline__ Frag<DT> load(const DT *row, int kk, int g4) {
         Frag<DT> f;
@@ -641,10 +638,10 @@ __device__ __forceinline__ int find_seq(const int32_t *cu, int N, int64_t total,
 // read its keys from one L2; the heads that are left over are dealt out tile by tile. Long
 // tiles (the last queries, which see the most keys) come first.
 struct HeadOrder {
-    int units, tiles, each, rest, first;  // heads in all, per XCD, left over; workgroups of those
+    int tiles, each, rest, first;  // heads per XCD, left over; workgroups of those
     static HeadOrder make(int64_t units, int64_t tiles) {
         const int64_t each = units / 8, rest = units % 8;
-        return HeadOrder{(int)units, (int)tiles, (int)each, (int)rest,
+        return HeadOrder{(int)tiles, (int)each, (int)rest,
                          (int)((rest * tiles + 7) / 8)};
     }
     int64_t grid() const { return 8 * ((int64_t)first + (int64_t)each * tiles); }

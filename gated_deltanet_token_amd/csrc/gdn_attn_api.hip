@@ -63,7 +63,8 @@ gdn_status_t attn_backward(const PromptArgs &a, const void *dout, const void *ou
     const bool packed = a.cu_count > 0;
     int cus = 0;
     if ((st = gdn::device_cus(&cus)) != GDN_OK) return st;
-    if (ws_bytes < backward_bytes(a, cus)) return GDN_ERR_BAD_SHAPE;
+    st = check_prompt_backward(a, dout, out, lse, dq, dk, dv, ws, ws_bytes, backward_bytes(a, cus));
+    if (st != GDN_OK) return st;
     if (packed && gdn::debug_checks(stream) &&
         (st = gdn::debug_cu_seqlens(a.cu, (int32_t)a.n, a.tokens, stream)) != GDN_OK)
         return st;
