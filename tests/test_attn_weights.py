@@ -190,6 +190,39 @@ def test_gradients_of_short_sequences_as_a_whole(gdn, D):
         assert off(x, w) < 4e-3, name
 
 
+@pytest.mark.parametrize("level", [2.0 ** 12, -2.0 ** 20, 1.5 * 2 ** 22])
+@pytest.mark.parametrize("K", [1, 5, 40])
+@pytest.mark.parametrize("dt,D", [("bf16", 64), ("bf16", 256), ("f32", 128)])
+def test_large_scores_against_the_cache(gdn, dt, D, K, level):
+    """The same against a cache, its parts joined: without a prefix, and with the first 96 tokens
+    as a prefix. Each of at most 32 parts is multiplied by 2^(m_i - m), one rounding and 2 U."""
+    n, Hq, Hk, page = 500, 4, 2, 16
+    q, k, v, _ = integers(D + K, n, Hq, Hk, D, level, DT[dt])
+    q = q[:, -K:].contiguous()
+    u, g = half_step(DT[dt]), Hq // Hk
+    pe = (2 * (2 * 24.0 + 6) + n + 32 + 3 * 32) * U32
+    seen = torch.arange(n) <= (n - K + torch.arange(K))[:, None]
+    pools = [t[0].contiguous() for t in (k, v)]
+    pools = [torch.cat([t, t.new_full((-n % page, Hk, D), math.nan)]).view(-1, page, Hk, D).to(DEV)
+             for t in pools]
+    table = torch.arange(pools[0].shape[0], dtype=torch.int32, device=DEV)[None]
+
+    def i32(*x):
+        return torch.tensor(x, dtype=torch.int32, device=DEV)
+    first = 96
+    calls = [(table, i32(n), {}),
+             (table[:, first // page:].contiguous(), i32(n - first),
+              {"prefix_table": table[:, :first // page].contiguous(), "prefix_lengths": i32(first),
+               "prefix_groups": i32(0, 1)})]
+    for pages, lengths, shared in calls:
+        out, _ = gdn.gdn_attn_decode(q.to(DEV), *pools, pages, lengths, scale=1.0, **shared)
+        for h in range(Hq):
+            a, b, c = q[0, :, h].double(), k[0, :, h // g].double(), v[0, :, h // g].double()
+            p = torch.softmax((a @ b.T).masked_fill(~seen, -math.inf), 1)
+            want = p @ c
+            within(out[0, :, h], want, (u + pe) * (p @ c.abs()) + u * want.abs(), (h, len(shared)))
+
+
 # ---------------------------------------------------------------- weights of 0
 
 
