@@ -20,9 +20,9 @@
 // type as operands of the products (bf16: off by 2^-9 to 2^-8 relative, like
 // the stored inputs), sums are fp32.
 //
-// Bound by the matrix instructions, busy 40 to 46 % of the time. 2 x 4,097 tokens of
-// 16/4 heads of 128: dq 231 us, dk and dv 345, statistics 14, join 22; with the
-// forward pass 719 us, 670 TFLOP/s counting 7 products in all.
+// Bound by the matrix instructions, busy 39 to 49 % of the time. 2 x 4,097 tokens of
+// 16/4 heads of 128: dq 212 us, dk and dv 337, statistics 14, join 22; with the
+// forward pass 719 to 728 us, 661 to 670 TFLOP/s counting 7 products in all.
 #include <type_traits>
 
 #include "gdn_attn.hpp"

@@ -21,7 +21,9 @@
 // the rows of a long run of new tokens. The tiles are those of the prompts' kernel
 // (gdn_attn_fwd.hip), dealt out in the same way. Bound by the matrix instructions: 64
 // sequences behind 32,768 shared tokens 83 us for 51 GFLOP, of whose row tiles a quarter is
-// empty (384 rows in tiles of 256); the whole call 113 us.
+// empty (384 rows in tiles of 256); the whole call 113 us. A piece of 512 tokens of each of 4
+// prompts behind 7,680 cached ones, 24/4 heads of 256: 425 us, 940 TFLOP/s; with nothing cached
+// 83 us, 156 TFLOP/s, since every row tile is dealt out as if it saw all keys.
 //
 // attn_join_kernel: the parts of every row, in a fixed order. Bound by latency: 32
 // parts of 1,536 rows 13 us (50 MB, 3.9 TB/s).
@@ -32,13 +34,16 @@ namespace gdn {
 namespace {
 
 // Rows per (sequence, key head) that attn_few_kernel takes. With 24 rows of 64 sequences of up
-// to 16,384 tokens (24/4 heads of 256, 4 new tokens) it takes 129 us, attn_rows_kernel 142; with
+// to 16,384 tokens (24/4 heads of 256, 4 new tokens) it takes 128 us, attn_rows_kernel 142; with
 // 32 fp32 rows of 32 sequences (16/4 heads of 128) 51 against 66. More rows do not fit its
 // registers.
 constexpr int kFewRows = 32;
 constexpr int kFewKeys = 32;   // keys per wave and step there
 constexpr int kFewTiles = 4;   // tiles of a workgroup at the least
-constexpr int kFewStart = 6;   // what starting and ending a unit costs, in tiles
+// What starting and ending a unit costs, in tiles: with 3, 6 and 12, 64 sequences of up to 16,384
+// tokens of 24/4 heads of 256 take 111, 101 and 102 us, of 16/4 heads of 64 36, 32 and 32; 64 of
+// up to 4,096 fp32 tokens of 16/4 heads of 128 49, 43 and 49.
+constexpr int kFewStart = 6;
 
 // The keys of a sequence, or of a prefix, in a paged cache, 16 at a time (pages hold whole
 // ones). operator() reads page numbers 64 at a time into a register and takes them from there
@@ -398,8 +403,13 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_few_kernel(DecodePlan d) {
 
 // Query rows against one run of keys: a group's against its prefix (PREFIX), or a sequence's
 // against its own.
-constexpr int kRowsStart = 20;            // places: a tile of keys takes 10
-constexpr int kRowsFull = 10, kRowsHalf = 7;  // and 7 where half of the rows or less are there
+// Places of a unit's start, and of a tile of keys where all or more than half of the rows are
+// there, or less. Taken from bf16 heads of 256 (64 sequences behind 32,768 shared tokens: start 10,
+// 20, 40: 114.6, 112.4, 114.0 us; half 5, 7, 10: 125, 112.4, 115.4) and used for all. Others would
+// gain up to 9 % from values of their own: 17 x 4 fp32 tokens of 128 78 us, with half 10 72; fp32
+// heads of 64 48 us, with start 40 44.5; bf16 heads of 128 49.3 us, with half 10 47.2.
+constexpr int kRowsStart = 20;
+constexpr int kRowsFull = 10, kRowsHalf = 7;
 constexpr int kRowsTiles = 4;             // tiles of a workgroup at the least
 struct RowRun {
     int first, rows, len;  // first sequence

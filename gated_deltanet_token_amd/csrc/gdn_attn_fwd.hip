@@ -7,9 +7,10 @@
 // One pass over the keys with a running reference and sum per query
 // (gdn_attn.hpp). Bound by the matrix instructions, beside them by LDS reads (a
 // fragment of keys or values feeds CT products) and the vector instructions of
-// the exponentials. 8,192 tokens of 24/4 heads of 256: 779 to 797 us, 1,035 to
+// the exponentials. 8,192 tokens of 24/4 heads of 256: 779 to 808 us, 1,020 to
 // 1,058 TFLOP/s, matrix instructions busy 49 % of the time; 2 x 8,192 of 16/4
-// heads of 128 513 us (1,071), of 64 317 us (868: more exponentials per product).
+// heads of 128 500 to 525 us (1,047 to 1,099), of 64 312 to 327 us (840 to 882: more
+// exponentials per product). fp32, 4,096 of 16/4 heads of 128: 662 us, 104 TFLOP/s.
 #include "gdn_attn.hpp"
 
 namespace gdn {
