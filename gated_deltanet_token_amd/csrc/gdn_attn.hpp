@@ -45,6 +45,12 @@ template <bool YES = true> __device__ __forceinline__ int fresh(int lane) {
 }
 template <typename DT, int D> constexpr bool kFresh = D * sizeof(DT) > 256;
 
+// Allows a kernel its dynamic LDS on the current device.
+template <typename K> hipError_t with_lds(K kernel, int bytes) {
+    return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                               hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 // A wave-uniform 64-bit value, in scalar registers (where the copies take their base).
 __device__ __forceinline__ int64_t uniform(int64_t x) {
     const uint32_t lo = __builtin_amdgcn_readfirstlane((int)x);

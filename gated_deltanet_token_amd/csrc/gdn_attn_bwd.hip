@@ -651,11 +651,6 @@ template <typename DT, int D> struct Shape {
     static constexpr int kBN = 4 * kKCT * 16;
 };
 
-template <typename K> hipError_t with_lds(K kernel, int bytes) {
-    return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                               hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
 template <typename DT, int D>
 hipError_t launch(const AttnBackwardParams &p, int cus, hipStream_t stream) {
     using S = Shape<DT, D>;

@@ -732,11 +732,6 @@ template <typename DT, int D> Layout layout(const AttnDecodeParams &p, int cus) 
     return o;
 }
 
-template <typename K> hipError_t with_lds(K kernel, int bytes) {
-    return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                               hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
 template <typename DT, int D, bool PREFIX>
 hipError_t launch_rows(const DecodePlan &d, hipStream_t stream) {
     using S = Shape<DT, D>;

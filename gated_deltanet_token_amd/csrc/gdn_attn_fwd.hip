@@ -77,9 +77,7 @@ hipError_t launch(const AttnParams &p, hipStream_t stream) {
         p.cu ? HeadOrder::make(p.Hq, p.total / BM + p.N)
              : HeadOrder::make((int64_t)p.N * p.Hq, (p.T + BM - 1) / BM);
     const auto kernel = attn_kernel<DT, D, CT, NW, BK, PER_SIMD>;
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize,
-                                             Tiles::kLds);
+    const hipError_t e = with_lds(kernel, Tiles::kLds);
     if (e != hipSuccess) return e;
     kernel<<<grid_of(order.grid(), 64 * NW), 64 * NW, Tiles::kLds, stream>>>(p, order);
     return hipGetLastError();
