@@ -11,7 +11,9 @@
 // scores of 2^20, whose differences fp32 still holds, and a factor of 2 at 2^23). A row's weights
 // share that factor. The dq kernel, which forms all of a row's weights, sums them, divides
 // its row by the sum and leaves 1 / sum for the weights in dk and dv (4 x 2,048 tokens of 16/4
-// heads of 64, forward and backward: 261 us, 258 without; 128 and 256 wide as fast).
+// heads of 64, forward and backward: 261 us, 258 without; 128 and 256 wide as fast). A sum further
+// from 1 than the rounding of lse explains is that of a row whose lse and out are over more keys
+// than these (a prefix in front, say): its weights stay as lse makes them.
 //
 // Three kernels: the rows' statistics; dq by query tiles (three products per pair
 // of tiles); dk and dv by key tiles (four). Scores and dout . v are formed in both:
@@ -82,6 +84,12 @@ template <typename DT> __device__ __forceinline__ void clear_odd(unsigned char *
         u32x4 &w = reinterpret_cast<u32x4 *>(t)[i];
         w = only_finite(w, DT{});
     }
+}
+
+// Whether a row's weights sum up to 1 but for the rounding of its lse (log2-scaled; three roundings
+// of 2^-24 each, and a fourth to spare) and of the sum.
+__device__ __forceinline__ bool whole_row(float all, float lse2) {
+    return all > 0.f && fabsf(log2f(all)) <= fmaf(fabsf(lse2), 0x1p-22f, 0x1p-16f);
 }
 
 template <typename DT, int D, int CT, int NW, int BK, int PER_SIMD>
@@ -179,7 +187,8 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void attn_dq_kernel(AttnBackward
                     }
                 all = across_sum(all);
                 of = across_sum(of);
-                delta[ct] = all == 0.f ? of : of / all;
+                if (!whole_row(all, lse[ct])) continue;
+                delta[ct] = of / all;
                 const int row = w0 + 16 * ct + c;
                 if (g4 == 0 && row < len)  // for dk and dv
                     p.stats[((int64_t)p.Hq + head) * p.total + tok0 + row] = delta[ct];
@@ -223,8 +232,7 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void attn_dq_kernel(AttnBackward
         const int row = w0 + 16 * ct + c;
         const float all = across_sum(sum[ct]);
         if (row >= len) continue;
-        // no weights at all, or NaN: as they are
-        const float f = all > 0.f ? 1.f / all : 1.f;
+        const float f = whole_row(all, lse[ct]) ? 1.f / all : 1.f;
         DT *o = static_cast<DT *>(p.dq) + ((tok0 + row) * p.Hq + head) * D + 4 * g4;
 #pragma unroll
         for (int dt = 0; dt < D / 16; ++dt) store4(o + 16 * dt, acc[dt][ct] * (p.scale * f));
@@ -413,7 +421,7 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void attn_dkv_kernel(AttnBackwar
 // once more as ds, dk came out 2.9e-3 off, relative to its norm, and not 2.4e-3; fp16 times 2^13
 // was as good for p above 2^-27 but nothing below 2^-38: keys that all queries nearly ignore lost
 // their dk; 2 x 4,097 tokens of 16/4 heads of 128, forward and backward: 728 us, so 720). p is at
-// most 1, its row's sum being 1; should it not be, it counts as just below 2.
+// most 1, its row's sum being 1 at the most; should it not be, it counts as just below 2.
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t code_of(float p) {  // in the upper half
     return (min(__builtin_bit_cast(uint32_t, p), 0x3FFFC000u) << 2) + 0x8000u;

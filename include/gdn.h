@@ -589,6 +589,8 @@ gdn_status_t gdn_attn_varlen_prefill(const void *q, const void *k, const void *v
  *
  * With p = exp(scale q_t . k_j - lse_t) and ds = p (dout_t . v_j - dout_t . out_t):
  *   dq_t = scale sum_j ds k_j,  dk_j = scale sum_t ds q_t,  dv_j = sum_t p dout_t.
+ * out and lse may be over more keys than these (a prefix in front, say): the
+ * results are then the part of these keys.
  * Results are the same from call to call. workspace:
  * gdn_attn_backward_workspace_size() bytes, required; for one call at a time.
  */

@@ -1,7 +1,7 @@
 """Weights at the ends of their range in attention and its gradients: scores so large that fp32
-holds them in steps of a quarter, weights so small that 16 bits lose them, weights of 0. Scores
-are sums of integers below 2^24 and exact in fp32 in any order, so the bounds of the tests of large
-ones hold no error of theirs."""
+holds them in steps of a quarter, weights so small that 16 bits lose them, weights that are a part
+of a row's, weights of 0. Scores are sums of integers below 2^24 and exact in fp32 in any order, so
+the bounds of the tests of large ones hold no error of theirs."""
 import math
 
 import pytest
@@ -221,6 +221,36 @@ def test_large_scores_against_the_cache(gdn, dt, D, K, level):
             p = torch.softmax((a @ b.T).masked_fill(~seen, -math.inf), 1)
             want = p @ c
             within(out[0, :, h], want, (u + pe) * (p @ c.abs()) + u * want.abs(), (h, len(shared)))
+
+
+# ------------------------------------------------- weights that are a part of a row's
+
+
+@pytest.mark.parametrize("P", [1, 40, 300])
+@pytest.mark.parametrize("dt,D", [("bf16", 64), ("bf16", 128), ("bf16", 256), ("f32", 64),
+                                  ("f32", 128), ("f32", 256)])
+def test_gradients_of_the_keys_behind_others(gdn, dt, D, P):
+    """The formulas hold with the out and lse of queries that see P keys more than are given: p and
+    delta are the whole row's. Against all P + T keys in 64 bits: dk and dv of the keys given, and
+    dq's part over them; the oracle's bounds of the whole sequence."""
+    T, Hq, Hk = 90, 4, 2
+    g = torch.Generator().manual_seed(D + P)
+    n, dtype = P + T, DT[dt]
+    q, do = (torch.randn(1, n, Hq, D, generator=g).to(dtype) for _ in range(2))
+    k, v = (torch.randn(1, n, Hk, D, generator=g).to(dtype) for _ in range(2))
+    qd, kd, vd, dd = dev(q, k, v, do)
+    out, lse = gdn.gdn_attn_prefill(qd, kd, vd, want_lse=True)
+    part = [t[:, P:].contiguous() for t in (dd, qd, kd, vd, out, lse)]
+    dq, dk, dv = gdn.gdn_attn_backward(*part)
+    want, tol = backward64(do[0], q[0], k[0], v[0], dtype)
+    within(dk[0], want[1][P:], tol[1][P:], "dk")
+    within(dv[0], want[2][P:], tol[2][P:], "dv")
+    for h in range(Hq):
+        a, b, c, d = (x[0, :, i].double() for x, i in ((q, h), (k, h // 2), (v, h // 2), (do, h)))
+        p = torch.softmax((a @ b.T * D ** -0.5).masked_fill(~causal(n), -math.inf), 1)
+        ds = p * (d @ c.T - (d * (p @ c)).sum(1, keepdim=True))
+        exact = (D ** -0.5 * ds[:, P:] @ b[P:])[P:]
+        within(dq[0, :, h], exact, tol[0][P:, h] + half_step(dtype) * exact.abs(), "dq")
 
 
 # ---------------------------------------------------------------- weights of 0
